@@ -1,4 +1,5 @@
-"""ctypes binding of libdspark.so: same entry points as include/dspark.h.
+"""ctypes binding of libdspark.so: same entry points as include/dspark.h and
+include/dspark_cache.h.
 
 This module only marshals arguments: torch tensors supply device pointers and
 torch supplies the current HIP stream.  Every step of the cycle runs in the
@@ -31,6 +32,12 @@ SYMBOLS = ("dspark_workspace_bytes", "dspark_status_string", "dspark_draft", "ds
            "dspark_sts_workspace_bytes", "dspark_sts_fit", "dspark_verify", "dspark_rnn_workspace_bytes",
            "dspark_draft_rnn", "dspark_verify_rnn", "dspark_schedule_noalloc",
            "dspark_probe_draws")
+# the paged cache (dspark_cache.h)
+CACHE_SYMBOLS = ("dspark_cache_workspace_bytes", "dspark_cache_append", "dspark_cache_attend", "dspark_cache_update",
+                 "dspark_cache_compact")
+F8E4M3 = 2  # cache_dtype only
+_CACHE_DT = {"f32": F32, "bf16": BF16, "f8": F8E4M3}
+_CACHE_TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16, F8E4M3: torch.float8_e4m3fn}
 
 
 class Problem(ctypes.Structure):
@@ -49,6 +56,32 @@ class Problem(ctypes.Structure):
     def from_config(cls, cfg) -> "Problem":
         return cls.make(cfg.B, cfg.K, cfg.V, cfg.r, cfg.d, cfg.logits_dtype, cfg.weight_dtype,
                         cfg.hidden_dtype, cfg.T_s, cfg.seed)
+
+
+class Cache(ctypes.Structure):
+    """Geometry and types of a paged cache (dspark_cache of dspark_cache.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "n_pages", "page", "max_pages", "n_layers", "Hq", "Hkv", "D",
+                                              "data_dtype", "cache_dtype")]
+
+    @classmethod
+    def make(cls, B, n_pages, page, max_pages, n_layers, Hq, Hkv, D, q="bf16", cache="bf16") -> "Cache":
+        return cls(B, n_pages, page, max_pages, n_layers, Hq, Hkv, D, _DT[q], _CACHE_DT[cache])
+
+    @property
+    def data_type(self) -> torch.dtype:
+        return _TORCH_DT[self.data_dtype]
+
+    @property
+    def cache_type(self) -> torch.dtype:
+        return _CACHE_TORCH_DT[self.cache_dtype]
+
+    @property
+    def k_shape(self):
+        return (self.n_layers, self.n_pages, self.Hkv, self.page, self.D)
+
+    @property
+    def v_shape(self):
+        return (self.n_layers, self.n_pages, self.Hkv, self.page // 8, self.D, 8)
 
 
 class DsparkError(RuntimeError):
@@ -121,6 +154,16 @@ def load(debug: bool | None = None) -> ctypes.CDLL:
     lib.dspark_debug_check_inputs.restype = i32
     lib.dspark_debug_force_barrier_timeout.argtypes = [i32]
     lib.dspark_debug_force_barrier_timeout.restype = i32
+    C, i64, f = ctypes.POINTER(Cache), ctypes.c_int64, ctypes.c_float
+    lib.dspark_cache_workspace_bytes.argtypes = [C, i32]
+    lib.dspark_cache_workspace_bytes.restype = sz
+    lib.dspark_cache_append.argtypes = [C, i32, vp, i64, vp, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.dspark_cache_attend.argtypes = [C, i32, vp, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, f, i32, i32, vp, i64,
+                                        vp, vp, sz, vp]
+    lib.dspark_cache_update.argtypes = [C] + [vp] * 12 + [sz, vp]
+    lib.dspark_cache_compact.argtypes = [C] + [vp] * 9 + [sz, vp]
+    for name in CACHE_SYMBOLS[1:]:
+        getattr(lib, name).restype = i32
     _libs[debug] = lib
     return lib
 
@@ -320,6 +363,128 @@ def verify_rnn(P: Problem, target, Z, E, Wt, anchor, draft_tok, draft_logq, draf
         _ptr(workspace, None, "workspace"), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
         _stream(stream))
     _check("dspark_verify_rnn", st)
+
+
+def cache_workspace_bytes(C: Cache, max_new: int) -> int:
+    return int(load().dspark_cache_workspace_bytes(ctypes.byref(C), int(max_new)))
+
+
+def _dev(t, dtype, shape, device, name, optional=False):
+    """Address of a dense device tensor of this dtype and shape on `device`; None passes NULL if optional."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, shape, device, name):
+    """(address, row stride) of [rows][heads][D] whose rows are dense but may lie apart."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    s = t.stride()
+    if s[2] != 1 or s[1] != shape[2]:
+        raise ValueError(f"{name}'s rows must be dense")
+    return t.data_ptr(), s[0]
+
+
+def _device(t):
+    """The device of the call: that of its tensors, which has to be the current one."""
+    d = t.device
+    if d.type != "cuda":
+        raise ValueError("the cache's tensors must be device tensors")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {d}, the current device is cuda:{torch.cuda.current_device()}")
+    return d
+
+
+def _workspace(t, device):
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def cache_append(C: Cache, layer: int, k, v, n_new, row_start, max_new: int, length, table, k_scale, v_scale,
+                 k_pool, v_pool, stream=None) -> None:
+    """The new tokens' keys and values (rows of k and v [rows][Hkv][D]) into layer `layer` of the pools."""
+    lib, dev = load(), _device(k_pool)
+    i32, f32, B, dt, ct = torch.int32, torch.float32, (C.B,), C.data_type, C.cache_type
+    rows = k.shape[0]
+    kp, ks = _rows(k, dt, (rows, C.Hkv, C.D), dev, "k")
+    vp, vs = _rows(v, dt, (rows, C.Hkv, C.D), dev, "v")
+    st = lib.dspark_cache_append(
+        C, layer, kp, ks, vp, vs, rows, _dev(n_new, i32, B, dev, "n_new", True),
+        _dev(row_start, i32, B, dev, "row_start", True), max_new, _dev(length, i32, B, dev, "length"),
+        _dev(table, i32, (C.B, C.max_pages), dev, "table"), _dev(k_scale, f32, (C.Hkv,), dev, "k_scale", True),
+        _dev(v_scale, f32, (C.Hkv,), dev, "v_scale", True), _dev(k_pool, ct, C.k_shape, dev, "k_pool"),
+        _dev(v_pool, ct, C.v_shape, dev, "v_pool"), _stream(stream))
+    _check("dspark_cache_append", st)
+
+
+def cache_attend(C: Cache, layer: int, q, n_new, row_start, max_new: int, length, table, k_pool, v_pool, k_scale,
+                 v_scale, out, lse, workspace, scale: float | None = None, causal: bool = True, window: int = 0,
+                 stream=None) -> None:
+    """Attention of the rows of q [rows][Hq][D] over their requests' pages; scale None is D ** -0.5."""
+    lib, dev = load(), _device(k_pool)
+    i32, f32, B, dt, ct = torch.int32, torch.float32, (C.B,), C.data_type, C.cache_type
+    rows = q.shape[0]
+    qp, qs = _rows(q, dt, (rows, C.Hq, C.D), dev, "q")
+    op, os_ = _rows(out, dt, (rows, C.Hq, C.D), dev, "out")
+    ws, nbytes = _workspace(workspace, dev)
+    st = lib.dspark_cache_attend(
+        C, layer, qp, qs, rows, _dev(n_new, i32, B, dev, "n_new", True), _dev(row_start, i32, B, dev, "row_start", True),
+        max_new, _dev(length, i32, B, dev, "length"), _dev(table, i32, (C.B, C.max_pages), dev, "table"),
+        _dev(k_pool, ct, C.k_shape, dev, "k_pool"), _dev(v_pool, ct, C.v_shape, dev, "v_pool"),
+        _dev(k_scale, f32, (C.Hkv,), dev, "k_scale", True), _dev(v_scale, f32, (C.Hkv,), dev, "v_scale", True),
+        C.D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, os_,
+        _dev(lse, f32, (rows, C.Hq), dev, "lse", True), ws, nbytes, _stream(stream))
+    _check("dspark_cache_attend", st)
+
+
+def cache_update(C: Cache, parent, new_len, table, length, ref, table_out, length_out, ref_out, n_short, k_pool, v_pool,
+                 workspace, stream=None) -> None:
+    """Every slot's next sequence: min(length[parent], new_len) tokens of its parent's, extended to new_len."""
+    lib, dev = load(), _device(k_pool)
+    i32, B, ct = torch.int32, (C.B,), C.cache_type
+    T, N = (C.B, C.max_pages), (C.n_pages,)
+    ws, nbytes = _workspace(workspace, dev)
+    st = lib.dspark_cache_update(
+        C, _dev(parent, i32, B, dev, "parent", True), _dev(new_len, i32, B, dev, "new_len"),
+        _dev(table, i32, T, dev, "table"), _dev(length, i32, B, dev, "length"), _dev(ref, i32, N, dev, "ref"),
+        _dev(table_out, i32, T, dev, "table_out"), _dev(length_out, i32, B, dev, "length_out"),
+        _dev(ref_out, i32, N, dev, "ref_out"), _dev(n_short, i32, (1,), dev, "n_short"),
+        _dev(k_pool, ct, C.k_shape, dev, "k_pool"), _dev(v_pool, ct, C.v_shape, dev, "v_pool"), ws, nbytes,
+        _stream(stream))
+    _check("dspark_cache_update", st)
+
+
+def cache_compact(C: Cache, table, length, ref, table_out, ref_out, n_live, k_pool, v_pool, workspace,
+                  stream=None) -> None:
+    """The live pages moved to the ids [0, n_live), with the table and the references renamed."""
+    lib, dev = load(), _device(k_pool)
+    i32, ct = torch.int32, C.cache_type
+    T, N = (C.B, C.max_pages), (C.n_pages,)
+    ws, nbytes = _workspace(workspace, dev)
+    st = lib.dspark_cache_compact(
+        C, _dev(table, i32, T, dev, "table"), _dev(length, i32, (C.B,), dev, "length"), _dev(ref, i32, N, dev, "ref"),
+        _dev(table_out, i32, T, dev, "table_out"), _dev(ref_out, i32, N, dev, "ref_out"),
+        _dev(n_live, i32, (1,), dev, "n_live"), _dev(k_pool, ct, C.k_shape, dev, "k_pool"),
+        _dev(v_pool, ct, C.v_shape, dev, "v_pool"), ws, nbytes, _stream(stream))
+    _check("dspark_cache_compact", st)
 
 
 def debug_flags(clear: bool = True) -> int:
