@@ -34,9 +34,11 @@ CFLAGS = [
 # Per-source additions.  The persistent draft keeps each wave's Wt fragments in
 # the accumulation registers (AGPRs) for the whole cycle; with the MFMA results
 # in ordinary registers its epilogue reads them directly (no accumulator copies)
-# and nothing spills.
+# and nothing spills.  The cache's attention likewise works on the MFMA results
+# with the vector ALUs in every key tile.
 SOURCE_FLAGS = {
     "k_persist.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "k_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

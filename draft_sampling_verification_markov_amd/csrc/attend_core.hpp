@@ -1,0 +1,554 @@
+// Paged-cache attention: what its kernels share -- operand types, the geometry of a
+// segment, the split of the work, the softmax of a tile, the join of partial results.
+//
+// Mathematics.  For a kv head, the G query heads that read it and the new tokens of
+// a request form the rows of one product: row rho = (token rho / G, head rho % G).
+// A tile of 32 keys gives S^T = K Q^T (32 keys x 32 rows) and O^T += V^T P^T with
+// P = exp2(c S - m), c the softmax scale times log2(e), m the row's running maximum,
+// l the running sum of P.  Transposed, a row is one MFMA column, that is one lane and
+// its partner 32 lanes on: the maximum and the sum of a row need one lane swap, a
+// rescaling of O is one factor per lane, and the registers that S^T leaves are, once
+// exponentiated and rounded, the B operand of the second product as they stand.  The
+// last holds because the rows of K are read in an order chosen for it (key_of): the
+// product sums over keys, so their order within the tile is free.
+//
+// Running maximum.  m only moves when some row's maximum rises by more than 2^8 in
+// weight; until then P may reach 2^8, which costs no precision (fp32 sums, and bf16
+// rounds relative to the value), and O is not rescaled.
+//
+// What a row does not see must not reach it, not even as NaN times a weight of 0.
+// Scores are replaced before the exponential.  In the tiles that some rows see in part
+// or not at all (the sequence's end, the diagonal, a window's edge) the values of keys
+// that no row sees, and all that are not finite, are replaced by 0; if a row does see
+// one that is not, the coordinate's result is made NaN or infinite when it is stored
+// (add_nonfinite), from the values themselves.  All other tiles are seen whole by all
+// rows and need no such care.
+#pragma once
+
+#include <type_traits>
+
+#include "dspark_cache_internal.hpp"
+
+namespace dspark {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2_t;
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr int kAttendThreads = 256;
+constexpr float kRescale = 8.f;  // log2 of the weight up to which the maximum may lag
+constexpr int kCUs = 256;
+
+// How the work of a call is dealt out.  A segment is one (item, kv head), an item one
+// row tile of one request; a unit is `unit` keys of a segment.  With `workers` 0 every
+// workgroup takes one whole segment; else the units of all segments, in order, are
+// dealt evenly to the workers, whose first and last segments may be partial.
+struct Split {
+  int row_tiles;  // of a request, at most
+  int workers;
+  int unit_shift;
+};
+
+// A partial segment: O (unnormalised) [rows][D], then (m, l) [rows]; two a worker.
+struct Record {  // of a worker whose first unit lies inside a segment (item -1: it does not)
+  int item, head;
+  int first, last;  // workers that share the segment
+  int slot;         // of the first one's part; the others' is twice their number
+};
+
+struct Geometry {
+  int b, row0, rows;      // request; first row of the tile among the request's; rows in it
+  int n, pos0;            // new tokens; position of token 0
+  int lo, hi;             // keys that some row sees
+  int all_lo, all_hi;     // keys in [all_lo, all_hi) are seen by every row
+  int tile0, tiles;       // units
+};
+
+struct Masks {
+  int causal, window, len;
+  __device__ __forceinline__ int hi(int pos) const { return causal ? max(0, min(len, pos + 1)) : len; }
+  __device__ __forceinline__ int lo(int pos) const { return window > 0 ? max(0, pos - window + 1) : 0; }
+};
+
+template <int ROWS>
+__device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int item) {
+  Geometry g;
+  const int G = a.c.Hq / a.c.Hkv;
+  g.b = p.row_tiles == 1 ? item : item / p.row_tiles;
+  const int rt = p.row_tiles == 1 ? 0 : item % p.row_tiles;
+  g.n = a.c.rows(g.b);
+  const int len = a.c.len(g.b);
+  g.pos0 = len - g.n;
+  g.row0 = rt * ROWS;
+  g.rows = min(ROWS, g.n * G - g.row0);
+  if (g.rows <= 0) {
+    g.rows = g.tiles = g.tile0 = g.lo = g.hi = g.all_lo = g.all_hi = 0;
+    return g;
+  }
+  const Masks m{a.causal, a.window, len};
+  const int first = g.pos0 + g.row0 / G, last = g.pos0 + (g.row0 + g.rows - 1) / G;
+  g.hi = m.hi(last);
+  g.lo = min(m.lo(first), g.hi);
+  g.all_hi = m.hi(first);
+  g.all_lo = m.lo(last);
+  g.tile0 = g.lo >> p.unit_shift;
+  g.tiles = max(1, ((g.hi + (1 << p.unit_shift) - 1) >> p.unit_shift) - g.tile0);  // 1: its rows are written
+  return g;
+}
+
+// Position in the dealt work: the segment that holds a worker's first unit.
+struct Start {
+  int item, head, skip;  // units of the segment before the worker's first
+  int count;             // the worker's units
+  int workers;           // that have any
+  long long unit, total;
+};
+
+__device__ __forceinline__ int wg_sum(int v, int* sh) {
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return sh[0] + sh[1] + sh[2] + sh[3];
+}
+
+// Every worker finds its own start: the units of all items are summed in chunks of
+// 256 (one item a thread), then the chunk that holds the start is searched.  For the
+// batches that are dealt (up to a few thousand items) that is cheaper than a launch
+// of its own.
+template <int ROWS>
+__device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p, int worker, int* sh) {
+  const int items = a.c.B * p.row_tiles;
+  __shared__ int found[2];
+  long long total = 0;
+  for (int c = 0; c < items; c += kAttendThreads) {
+    const int i = c + threadIdx.x;
+    total += wg_sum(i < items ? geometry<ROWS>(a, p, i).tiles : 0, sh);
+  }
+  const int Hkv = a.c.Hkv;
+  Start s;
+  s.total = total * Hkv;
+  s.workers = (int)(s.total < p.workers ? s.total : p.workers);
+  s.unit = s.workers ? worker * s.total / s.workers : 0;
+  s.count = worker < s.workers ? (int)((worker + 1) * s.total / s.workers - s.unit) : 0;
+  s.item = s.head = s.skip = 0;
+  if (s.count == 0) return s;
+  long long before = 0;
+  for (int c = 0; c < items; c += kAttendThreads) {
+    const int i = c + threadIdx.x;
+    const int t = i < items ? geometry<ROWS>(a, p, i).tiles : 0;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int x = t;
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) sh[wave] = x;
+    __syncthreads();
+    int base = 0, all = 0;
+    for (int w = 0; w < kAttendThreads / 64; ++w) {
+      if (w < wave) base += sh[w];
+      all += sh[w];
+    }
+    const long long u0 = (before + base + x - t) * Hkv;
+    if (s.unit < (before + all) * Hkv) {  // in this chunk
+      if (t > 0 && s.unit >= u0 && s.unit < u0 + (long long)t * Hkv) {
+        found[0] = i;
+        found[1] = (int)(s.unit - u0);
+      }
+      __syncthreads();
+      s.item = found[0];
+      const int tiles = geometry<ROWS>(a, p, s.item).tiles;
+      s.head = found[1] / tiles;
+      s.skip = found[1] % tiles;
+      return s;
+    }
+    before += all;
+  }
+  return s;
+}
+
+// A request's row of the page table, read over the scalar cache (uniform addresses).
+struct TableRow {
+  const __attribute__((address_space(4))) int32_t* row;
+  int shift, last, n_pages;
+  __device__ __forceinline__ TableRow(const CacheView& c, int b)
+      : row((const __attribute__((address_space(4))) int32_t*)(uintptr_t)(c.table + (size_t)b * c.max_pages)),
+        shift(c.page_shift), last(c.max_pages - 1), n_pages(c.n_pages) {}
+  __device__ __forceinline__ int raw(int key) const { return row[min(key >> shift, last)]; }
+  __device__ __forceinline__ unsigned id(int raw) const { return min((unsigned)raw, (unsigned)n_pages - 1u); }
+};
+
+// ---- operands
+// Element types of the two products: bf16 MFMA for bf16 and e4m3 caches (an e4m3
+// value is a bf16 value; its scale is a factor of the scores and of the result),
+// fp32 MFMA for fp32.
+template <int CT>
+struct Operand {
+  static constexpr bool kF32 = CT == DSPARK_F32;
+  static constexpr int kBytes = CT == DSPARK_F32 ? 4 : CT == DSPARK_BF16 ? 2 : 1;
+  using Data = typename std::conditional<kF32, float, uint16_t>::type;
+};
+
+__device__ __forceinline__ bf16x8_t as_bf16x8(uint4 w) { return __builtin_bit_cast(bf16x8_t, w); }
+__device__ __forceinline__ bf16x8_t f8_to_bf16x8(uint32_t lo, uint32_t hi) {
+  bf16x2_t r[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true),
+                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true)};
+  bf16x8_t o;
+  __builtin_memcpy(&o, r, 16);
+  return o;
+}
+__device__ __forceinline__ f32x16_t mma(bf16x8_t x, bf16x8_t y, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma(float x, float y, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(x, y, c, 0, 0, 0);
+}
+__device__ __forceinline__ float lane4(const uint4& w, int e) {
+  return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
+}
+
+// Row m of the K operand holds this key of the tile.  S^T row m = 8 j + 4 h + i sits in
+// register 4 j + i of half-wave h; the bf16 product takes 8 consecutive keys of a
+// 16-key slab from each half, so those rows are the keys 16 (j / 2) + 8 h + 4 (j % 2) + i.
+// The fp32 product takes one key of each half at a time: rows are keys.
+template <bool F32>
+__device__ __forceinline__ int key_of_row(int m) {
+  if (F32) return m;
+  const int j = m >> 3, h = (m >> 2) & 1, i = m & 3;
+  return 16 * (j >> 1) + 8 * h + 4 * (j & 1) + i;
+}
+// The key of score register r in half-wave h.
+template <bool F32>
+__device__ __forceinline__ constexpr int key_of_reg(int r, int h) {
+  return F32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 16 * (r >> 3) + 8 * h + (r & 7);
+}
+
+// A lane's part of a 32-key tile: K row (l % 32) and, for each 32 coordinates, the
+// values of its keys.  16-byte loads throughout.
+//   bf16: K register x holds d = 16 x + 8 h ..; V register (s, db) the keys 16 s + 8 h ..
+//   e4m3: K register x holds d = 32 x + 16 h ..; V (s, db) 8 bytes
+//   fp32: K register x holds d = 8 x + 4 h ..; V (j, db) the keys 8 j + 4 h ..
+template <int CT, int D>
+struct Tile {
+  static constexpr bool kF32 = CT == DSPARK_F32;
+  static constexpr int kK = CT == DSPARK_F32 ? D / 8 : CT == DSPARK_BF16 ? D / 16 : D / 32;  // uint4
+  static constexpr int kSlabs = kF32 ? 4 : 2;
+  static constexpr int kBlocks = D / 32;
+  using V = typename std::conditional<CT == DSPARK_F8E4M3, uint2, uint4>::type;
+};
+
+// The first coordinate that half h of Q (and K) register x holds; of 8 (bf16 operand)
+// or 4 (fp32) consecutive ones.
+template <int CT>
+__device__ __forceinline__ constexpr int coord(int x, int h) {
+  return CT == DSPARK_F32 ? 8 * x + 4 * h : CT == DSPARK_BF16 ? 16 * x + 8 * h : 32 * (x >> 1) + 16 * h + 8 * (x & 1);
+}
+template <int CT, int D>
+constexpr int q_regs() { return CT == DSPARK_F32 ? D / 8 : D / 16; }
+
+// S^T of one 32-row block
+template <int CT, int D>
+__device__ __forceinline__ f32x16_t scores(const uint4 (&k)[Tile<CT, D>::kK], const uint4 (&q)[q_regs<CT, D>()]) {
+  f32x16_t s = {};
+#pragma unroll
+  for (int x = 0; x < Tile<CT, D>::kK; ++x) {
+    if constexpr (CT == DSPARK_F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = mma(lane4(k[x], e), lane4(q[x], e), s);
+    } else if constexpr (CT == DSPARK_BF16) {
+      s = mma(as_bf16x8(k[x]), as_bf16x8(q[x]), s);
+    } else {
+      s = mma(f8_to_bf16x8(k[x].x, k[x].y), as_bf16x8(q[2 * x]), s);
+      s = mma(f8_to_bf16x8(k[x].z, k[x].w), as_bf16x8(q[2 * x + 1]), s);
+    }
+  }
+  return s;
+}
+
+// One row's running state in a lane: m is common to the row's two lanes, l is the
+// lane's share of the sum.
+struct Running {
+  float m, l;
+};
+
+// Leaves the scores of the tile's keys that the row sees (lo <= key < hi).
+template <bool F32>
+__device__ __forceinline__ void mask_scores(f32x16_t& s, int lo, int hi, int h) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int key = key_of_reg<F32>(i, h);
+    s[i] = key >= lo && key < hi ? s[i] : -INFINITY;
+  }
+}
+
+// Weights of a tile from its scores; returns the factor by which O and l fade (1 for
+// most tiles).
+__device__ __forceinline__ float weights(f32x16_t& s, Running& r, float c) {
+  float top = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+  top = halves32_max(top) * c;
+  float fade = 1.f;
+  if (__any(top > r.m + kRescale)) {
+    const float m = fmaxf(r.m, top);
+    fade = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
+    r.m = m;
+    r.l *= fade;
+  }
+  const float ref = r.m == -INFINITY ? 0.f : r.m;
+  float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
+    s[i + 1] = __builtin_amdgcn_exp2f(fmaf(s[i + 1], c, -ref));
+    sum0 += s[i];
+    sum1 += s[i + 1];
+  }
+  r.l += sum0 + sum1;
+  return fade;
+}
+
+__device__ __forceinline__ bf16x8_t pack8(const f32x16_t& s, int at) {
+  bf16x8_t o;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const bf16x2_t p = __builtin_convertvector(f32x2_t{s[at + i], s[at + i + 1]}, bf16x2_t);
+    o[i] = p[0];
+    o[i + 1] = p[1];
+  }
+  return o;
+}
+
+// ---- values that a tile's rows see in part or not at all
+template <int CT>
+__device__ __forceinline__ uint32_t finite_word(uint32_t w) {
+  if constexpr (CT == DSPARK_F32) {
+    return (w & 0x7F800000u) == 0x7F800000u ? 0u : w;
+  } else if constexpr (CT == DSPARK_BF16) {
+    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+  } else {
+    uint32_t o = w;
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+      if ((w >> e & 0x7Fu) == 0x7Fu) o &= ~(0xFFu << e);
+    return o;
+  }
+}
+// Keeps the finite elements of `x` (consecutive keys from key0 on) with key in
+// [lo, hi); true if another one of those keys was there.
+template <int CT, typename V>
+__device__ __forceinline__ bool keep_keys(V& x, int key0, int lo, int hi) {
+  constexpr int kWords = sizeof(V) / 4, kPer = CT == DSPARK_F32 ? 1 : CT == DSPARK_BF16 ? 2 : 4, kBits = 32 / kPer;
+  uint32_t w[kWords];
+  __builtin_memcpy(w, &x, sizeof(V));
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int key = key0 + i * kPer + e;
+      if (key >= lo && key < hi) mask |= kPer == 1 ? ~0u : ((1u << (kBits & 31)) - 1) << (e * kBits);
+    }
+    const uint32_t seen = w[i] & mask;
+    w[i] = finite_word<CT>(seen);
+    odd = odd || w[i] != seen;
+  }
+  __builtin_memcpy(&x, w, sizeof(V));
+  return odd;
+}
+
+// O^T += V^T P^T of one 32-row block
+template <int CT, int D>
+__device__ __forceinline__ void add_values(const typename Tile<CT, D>::V (&v)[Tile<CT, D>::kSlabs][D / 32],
+                                           const f32x16_t& w, f32x16_t (&acc)[D / 32]) {
+  if constexpr (CT == DSPARK_F32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int db = 0; db < D / 32; ++db) acc[db] = mma(lane4(v[j][db], e), w[4 * j + e], acc[db]);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const bf16x8_t p = pack8(w, 8 * s);
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db) {
+        if constexpr (CT == DSPARK_BF16)
+          acc[db] = mma(as_bf16x8(v[s][db]), p, acc[db]);
+        else
+          acc[db] = mma(f8_to_bf16x8(v[s][db].x, v[s][db].y), p, acc[db]);
+      }
+    }
+  }
+}
+
+// ---- results
+// out and lse of one row from its sums
+__device__ __forceinline__ float row_factor(float l, float vs) { return l == 0.f ? 0.f : vs / l; }
+
+template <int CT>
+__device__ __forceinline__ void store4(void* out, size_t at, float4 y) {
+  if constexpr (CT == DSPARK_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = y;
+  } else {
+    uint2 w;
+    const bf16x2_t p = __builtin_convertvector(f32x2_t{y.x, y.y}, bf16x2_t);
+    const bf16x2_t q = __builtin_convertvector(f32x2_t{y.z, y.w}, bf16x2_t);
+    __builtin_memcpy(&w.x, &p, 4);
+    __builtin_memcpy(&w.y, &q, 4);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
+  }
+}
+
+template <int CT>
+__device__ __forceinline__ float cached(const char* p) {
+  if constexpr (CT == DSPARK_F32)
+    return *reinterpret_cast<const float*>(p);
+  else if constexpr (CT == DSPARK_BF16)
+    return bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
+  else
+    return __builtin_amdgcn_cvt_f32_fp8(*reinterpret_cast<const uint8_t*>(p), 0);
+}
+
+// What the values that are not finite make of coordinates d .. d + 3 of the row at
+// position pos: those of the keys in [k0, k1) outside [all_lo, all_hi) that it sees.
+template <int CT, int D>
+__device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometry& g, const Masks& mask, int head,
+                                              int pos, int d, int k0, int k1, float4& y) {
+  const CacheView& c = a.c;
+  const int lo = max(k0, mask.lo(pos)), hi = min(k1, mask.hi(pos));
+  for (int key = lo; key < hi; ++key) {
+    if (key >= g.all_lo && key < g.all_hi) continue;
+    const unsigned page = min((unsigned)c.table[(size_t)g.b * c.max_pages + (key >> c.page_shift)], (unsigned)c.n_pages - 1u);
+    const size_t token = (((size_t)page * c.Hkv + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+    const char* src = static_cast<const char*>(a.v_pool) +
+                      ((token & ~(size_t)7) * D + (size_t)d * 8 + (token & 7)) * Operand<CT>::kBytes;
+    float* const out = &y.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = cached<CT>(src + i * 8 * Operand<CT>::kBytes);
+      if (!(fabsf(x) < INFINITY)) out[i] += x;
+    }
+  }
+}
+
+constexpr float kLn2f = 0.6931471805599453f;
+
+// Row rho of the tile: its row of q and out, or -1
+__device__ __forceinline__ long long global_row(const AttendArgs& a, const Geometry& g, int rho, int head, int& hq) {
+  const int G = a.c.Hq / a.c.Hkv;
+  const int t = (g.row0 + rho) / G;
+  hq = head * G + (g.row0 + rho) - t * G;
+  const long long r = a.c.first_row(g.b) + t;
+  return a.c.has_row(r) ? r : -1;
+}
+
+template <int D>
+constexpr size_t slot_floats(int rows) { return (size_t)rows * (D + 2); }
+
+inline size_t records_bytes(int workers) { return align256((size_t)workers * sizeof(Record)); }
+
+// The workspace of a dealt call
+struct Partials {
+  Record* records;
+  float* slots;
+  template <int D, int ROWS>
+  __device__ __forceinline__ float* slot(int i) const { return slots + (size_t)i * slot_floats<D>(ROWS); }
+};
+__device__ __forceinline__ Partials partials(const AttendArgs& a, const Split& p) {
+  return {static_cast<Record*>(a.workspace),
+          reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align256((size_t)p.workers * sizeof(Record)))};
+}
+
+// Worker `worker`'s record (one thread writes it)
+__device__ __forceinline__ void put_record(const Partials& ws, const Start& s, int worker, int tiles) {
+  Record r{-1, 0, 0, 0, 0};
+  if (s.count > 0 && s.skip > 0) {
+    const long long u0 = s.unit - s.skip;  // a unit u is worker ((u + 1) W - 1) / total's
+    r.item = s.item;
+    r.head = s.head;
+    r.first = (int)(((u0 + 1) * s.workers - 1) / s.total);
+    r.last = (int)(((u0 + tiles) * s.workers - 1) / s.total);
+    r.slot = 2 * r.first + (r.first * s.total / s.workers == u0 ? 0 : 1);
+  }
+  ws.records[worker] = r;
+}
+
+// Joins the partial results of the segment that worker blockIdx.x's first unit lies
+// in, if the worker is the segment's second one; 8 rows a workgroup.  A row's parts
+// (m, l, O) add up as sum exp2(m - M) (l, O).  With few parts a group of threads
+// takes a row, with many all groups take a row's parts in turn (joined in a fixed
+// order).
+template <int CT, int D, int ROWS>
+__global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Split p) {
+  constexpr int kLanes = D / 4, kGroups = kAttendThreads / kLanes;  // a float4 a lane
+  const Partials ws = partials(a, p);
+  const Record rec = ws.records[blockIdx.x];
+  if (rec.item < 0 || (int)blockIdx.x != rec.first + 1) return;
+  const Geometry g = geometry<ROWS>(a, p, rec.item);
+  const int group = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4;
+  const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
+  const int parts = rec.last - rec.first + 1;
+  auto slot = [&](int i) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };
+  __shared__ float sm[kGroups], sl[kGroups];
+  __shared__ float4 so[kGroups][kLanes];
+  const bool by_row = parts <= 8;
+  for (int r0 = blockIdx.y * 8; r0 < g.rows && r0 < (int)(blockIdx.y + 1) * 8; r0 += by_row ? kGroups : 1) {
+    const int rho = by_row ? r0 + group : r0;
+    const bool on = rho < g.rows && rho < (int)(blockIdx.y + 1) * 8;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on)
+      for (int i = by_row ? 0 : group; i < parts; i += by_row ? 1 : kGroups) {
+        const float* s = slot(i);
+        const float2 ml = *reinterpret_cast<const float2*>(s + (size_t)ROWS * D + 2 * rho);
+        const float4 x = *reinterpret_cast<const float4*>(s + (size_t)rho * D + d);
+        const float top = fmaxf(m, ml.x);
+        const float f0 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+        const float f1 = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+        // a part without visible keys has m = -inf, l = 0, O = 0; NaN parts have a NaN l
+        l = l * f0 + (ml.x == -INFINITY ? ml.y : ml.y * f1);
+        o.x = o.x * f0 + x.x * f1;
+        o.y = o.y * f0 + x.y * f1;
+        o.z = o.z * f0 + x.z * f1;
+        o.w = o.w * f0 + x.w * f1;
+        m = top;
+      }
+    if (!by_row) {
+      __syncthreads();
+      so[group][threadIdx.x % kLanes] = o;
+      if (d == 0) {
+        sm[group] = m;
+        sl[group] = l;
+      }
+      __syncthreads();
+      if (group != 0) continue;
+      for (int i = 1; i < kGroups; ++i) {
+        const float top = fmaxf(m, sm[i]);
+        const float f0 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+        const float f1 = sm[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[i] - top);
+        const float4 x = so[i][threadIdx.x % kLanes];
+        l = l * f0 + (sm[i] == -INFINITY ? sl[i] : sl[i] * f1);
+        o.x = o.x * f0 + x.x * f1;
+        o.y = o.y * f0 + x.y * f1;
+        o.z = o.z * f0 + x.z * f1;
+        o.w = o.w * f0 + x.w * f1;
+        m = top;
+      }
+    }
+    if (!on) continue;
+    int hq;
+    const long long row = global_row(a, g, rho, rec.head, hq);
+    if (row < 0) continue;
+    const float f = row_factor(l, vs);
+    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    store4<CT>(a.out, row * a.out_stride + (size_t)hq * D + d, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+    if (a.lse && d == 0) a.lse[row * a.c.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
+  }
+}
+
+}  // namespace dspark

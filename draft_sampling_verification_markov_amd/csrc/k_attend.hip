@@ -1,99 +1,73 @@
-// Paged cache: attention of each request's new tokens over its pages.  See
-// include/dspark_cache.h for the contract.
-#include "dspark_cache_internal.hpp"
+// Paged cache: attention of each request's new tokens over its pages -- the choice of
+// kernel and split.  See include/dspark_cache.h for the contract, attend_core.hpp for
+// the mathematics.
+#include "attend_keys.hpp"
 
 namespace dspark {
 namespace {
 
-template <int CT>
-__device__ __forceinline__ float load_cached(const void* p, size_t i) {
-  if constexpr (CT == DSPARK_F32)
-    return static_cast<const float*>(p)[i];
-  else if constexpr (CT == DSPARK_BF16)
-    return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  else
-    return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p)[i], 0);
+// Workgroups that the chip holds at once decide how many workers share the units.
+struct Plan {
+  Split split;
+  int rows;     // of a tile
+  int slots;    // partial results
+};
+
+constexpr int kDirectKeys = 1024;
+
+int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / C.Hkv); }
+
+Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int occupancy) {
+  Plan pl{};
+  pl.rows = rows;
+  pl.split.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
+  pl.split.unit_shift = unit_shift;
+  long long keys = (long long)C.max_pages * C.page;
+  if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
+  const long long segments = (long long)C.B * pl.split.row_tiles * C.Hkv;
+  // few keys a segment: nothing to share out
+  const bool direct = keys <= kDirectKeys && segments <= (1 << 22);
+  pl.split.workers = direct ? 0 : kCUs * occupancy;
+  return pl;
 }
 
-// One wave a (row, query head): 64 positions at a time, one a lane, with the
-// running maximum and sum of the softmax; then every lane adds the 64 weighted
-// values of its D / 64 coordinates.
-template <int CT, int D>
-__global__ __launch_bounds__(64) void k_attend_rows(AttendArgs a) {
-  const CacheView& c = a.c;
-  const int b = blockIdx.x / c.max_new, i = blockIdx.x % c.max_new, hq = blockIdx.y, lane = threadIdx.x;
-  const int n = c.rows(b), len = c.len(b);
-  const long long row = c.first_row(b) + i;
-  if (i >= n || !c.has_row(row)) return;
-  const int head = hq / (c.Hq / c.Hkv);
-  const float ks = CT == DSPARK_F8E4M3 ? a.k_scale[head] : 1.f, vs = CT == DSPARK_F8E4M3 ? a.v_scale[head] : 1.f;
-  const int pos = len - n + i;
-  const int hi = a.causal && pos + 1 < len ? pos + 1 : len;
-  const int lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-  __shared__ float q[D];
-  for (int d = lane; d < D; d += 64)
-    q[d] = load_cached<CT == DSPARK_F32 ? DSPARK_F32 : DSPARK_BF16>(a.q, row * a.q_stride + (size_t)hq * D + d);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[D / 64] = {};
-  for (int j0 = lo; j0 < hi; j0 += 64) {
-    const int j = j0 + lane;
-    float x = -INFINITY;
-    if (j < hi) {
-      const int page = min((unsigned)c.table[(size_t)b * c.max_pages + (j >> c.page_shift)], (unsigned)c.n_pages - 1);
-      const size_t at = ((((size_t)page * c.Hkv + head) << c.page_shift) + (j & ((1 << c.page_shift) - 1))) * D;
-      float dot = 0.f;
-      for (int d = 0; d < D; ++d) dot += q[d] * load_cached<CT>(a.k_pool, at + d);
-      x = dot * ks * a.scale2;
-    }
-    const float top = fmaxf(m, wave_max(x));
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float p = j < hi ? __builtin_amdgcn_exp2f(x - ref) : 0.f;
-    const float fade = __builtin_amdgcn_exp2f(m - ref);
-    l = l * fade + wave_sum(p);
-    for (int e = 0; e < D / 64; ++e) o[e] *= fade;
-    m = top;
-    for (int t = 0; t < 64 && j0 + t < hi; ++t) {
-      const int jt = j0 + t;
-      const int page = min((unsigned)c.table[(size_t)b * c.max_pages + (jt >> c.page_shift)], (unsigned)c.n_pages - 1);
-      const int off = jt & ((1 << c.page_shift) - 1);
-      const size_t at = ((((size_t)page * c.Hkv + head) << c.page_shift) + (off & ~7)) * D + (off & 7);
-      const float w = __shfl(p, t);
-      for (int e = 0; e < D / 64; ++e) o[e] += w * load_cached<CT>(a.v_pool, at + (size_t)(e * 64 + lane) * 8);
-    }
+template <int CT, int D, int NB, int OCC>
+hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
+  const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 32, 7, OCC);
+  if (!pl.split.workers) {
+    k_attend_keys<CT, D, NB, OCC><<<C.B * pl.split.row_tiles * C.Hkv, kAttendThreads, 0, s>>>(a, pl.split);
+    return hipGetLastError();
   }
-  const float inv = l > 0.f ? vs / l : l == 0.f ? 0.f : l;  // NaN stays
-  for (int e = 0; e < D / 64; ++e) {
-    const float y = l == 0.f ? 0.f : o[e] * inv;
-    const size_t at = row * a.out_stride + (size_t)hq * D + e * 64 + lane;
-    if constexpr (CT == DSPARK_F32)
-      static_cast<float*>(a.out)[at] = y;
-    else
-      static_cast<uint16_t*>(a.out)[at] = (uint16_t)f32_to_bf16_bits(y);
-  }
-  if (a.lse && lane == 0) a.lse[row * c.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
-template <int CT>
-hipError_t attend_typed(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)C.B * a.c.max_new, C.Hq);
-  if (C.D == 64)
-    k_attend_rows<CT, 64><<<grid, 64, 0, s>>>(a);
-  else if (C.D == 128)
-    k_attend_rows<CT, 128><<<grid, 64, 0, s>>>(a);
-  else
-    k_attend_rows<CT, 256><<<grid, 64, 0, s>>>(a);
+  k_attend_keys<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, NB * 32><<<dim3(pl.split.workers, NB * 4), kAttendThreads, 0, s>>>(a, pl.split);
   return hipGetLastError();
+}
+
+template <int CT, int D>
+hipError_t run(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
+  const int rows = max_rows(C, a.c.max_new);
+  constexpr int kOne = CT != DSPARK_F32 && D <= 128 ? 2 : 1;
+  if (rows <= 32 || D == 256) return run_keys<CT, D, 1, kOne>(C, a, s);
+  return run_keys<CT, D, D == 256 ? 1 : 2, 1>(C, a, s);
+}
+
+template <int CT>
+hipError_t run_type(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
+  return C.D == 64 ? run<CT, 64>(C, a, s) : C.D == 128 ? run<CT, 128>(C, a, s) : run<CT, 256>(C, a, s);
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(const dspark_cache&, int32_t) { return 0; }
+size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new) {
+  // two partial results a worker, at most 64 rows and 2 workers a CU
+  return records_bytes(2 * kCUs) + (size_t)2 * 2 * kCUs * 64 * (C.D + 2) * sizeof(float);
+}
 
 hipError_t launch_cache_attend(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   switch (C.cache_dtype) {
-    case DSPARK_F32: return attend_typed<DSPARK_F32>(C, a, s);
-    case DSPARK_BF16: return attend_typed<DSPARK_BF16>(C, a, s);
-    default: return attend_typed<DSPARK_F8E4M3>(C, a, s);
+    case DSPARK_F32: return run_type<DSPARK_F32>(C, a, s);
+    case DSPARK_BF16: return run_type<DSPARK_BF16>(C, a, s);
+    default: return run_type<DSPARK_F8E4M3>(C, a, s);
   }
 }
 
