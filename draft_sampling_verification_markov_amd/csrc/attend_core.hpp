@@ -336,28 +336,48 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
     return o;
   }
 }
-// Keeps the finite elements of `x` (consecutive keys from key0 on) with key in
-// [lo, hi); true if another one of those keys was there.
+// Of a lane's 16 (8, e4m3) bytes of values, consecutive keys from key0 on: the bits of
+// the keys in [lo, hi).
 template <int CT, typename V>
-__device__ __forceinline__ bool keep_keys(V& x, int key0, int lo, int hi) {
-  constexpr int kWords = sizeof(V) / 4, kPer = CT == DSPARK_F32 ? 1 : CT == DSPARK_BF16 ? 2 : 4, kBits = 32 / kPer;
+struct KeyMask {
+  static constexpr int kWords = sizeof(V) / 4, kPer = CT == DSPARK_F32 ? 1 : CT == DSPARK_BF16 ? 2 : 4;
   uint32_t w[kWords];
-  __builtin_memcpy(w, &x, sizeof(V));
-  bool odd = false;
+  __device__ __forceinline__ KeyMask(int key0, int lo, int hi) {
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    uint32_t mask = 0;
+    for (int i = 0; i < kWords; ++i) {
+      w[i] = 0;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int key = key0 + i * kPer + e;
-      if (key >= lo && key < hi) mask |= kPer == 1 ? ~0u : ((1u << (kBits & 31)) - 1) << (e * kBits);
+      for (int e = 0; e < kPer; ++e) {
+        const int key = key0 + i * kPer + e;
+        if (key >= lo && key < hi) w[i] |= kPer == 1 ? ~0u : ((1u << (32 / kPer & 31)) - 1) << (e * (32 / kPer));
+      }
     }
-    const uint32_t seen = w[i] & mask;
-    w[i] = finite_word<CT>(seen);
-    odd = odd || w[i] != seen;
   }
+  // x without the other keys; kOdd bits are left in `odd` if an element is not finite
+  // (all exponent bits set, e4m3: all bits but the sign: adding one carries into the
+  // element's top bit)
+  static constexpr uint32_t kOdd = CT == DSPARK_F32 ? 0x80000000u : CT == DSPARK_BF16 ? 0x80008000u : 0x80808080u;
+  __device__ __forceinline__ void apply(V& x, uint32_t& odd) const {
+    constexpr uint32_t kExp = CT == DSPARK_F32 ? 0x7F800000u : CT == DSPARK_BF16 ? 0x7F807F80u : 0x7F7F7F7Fu;
+    constexpr uint32_t kOne = CT == DSPARK_F32 ? 0x00800000u : CT == DSPARK_BF16 ? 0x00800080u : 0x01010101u;
+    uint32_t y[kWords];
+    __builtin_memcpy(y, &x, sizeof(V));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      y[i] &= w[i];
+      odd |= (y[i] & kExp) + kOne;
+    }
+    __builtin_memcpy(&x, y, sizeof(V));
+  }
+};
+template <int CT, typename V>
+__device__ __forceinline__ V finite_part(V x) {
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &x, sizeof(V));
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i) w[i] = finite_word<CT>(w[i]);
   __builtin_memcpy(&x, w, sizeof(V));
-  return odd;
+  return x;
 }
 
 // O^T += V^T P^T of one 32-row block
@@ -479,75 +499,99 @@ __device__ __forceinline__ void put_record(const Partials& ws, const Start& s, i
 }
 
 // Joins the partial results of the segment that worker blockIdx.x's first unit lies
-// in, if the worker is the segment's second one; 8 rows a workgroup.  A row's parts
-// (m, l, O) add up as sum exp2(m - M) (l, O).  With few parts a group of threads
-// takes a row, with many all groups take a row's parts in turn (joined in a fixed
-// order).
+// in, if the worker is the segment's second one.  A row's parts (m, l, O) add up as
+// sum exp2(m - M) (l, O), M the largest m, in a fixed order.  Few parts: a group of
+// D / 4 threads takes a row, 8 rows a workgroup.  Many (a long context dealt to many
+// workers): the workgroup takes a row, its groups the parts in turn.
+constexpr int kJoinY = 8;
+constexpr int kFewParts = 8;
 template <int CT, int D, int ROWS>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Split p) {
   constexpr int kLanes = D / 4, kGroups = kAttendThreads / kLanes;  // a float4 a lane
   const Partials ws = partials(a, p);
   const Record rec = ws.records[blockIdx.x];
   if (rec.item < 0 || (int)blockIdx.x != rec.first + 1) return;
-  const Geometry g = geometry<ROWS>(a, p, rec.item);
-  const int group = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4;
-  const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
   const int parts = rec.last - rec.first + 1;
+  const Geometry g = geometry<ROWS>(a, p, rec.item);
+  const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
   auto slot = [&](int i) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };
-  __shared__ float sm[kGroups], sl[kGroups];
-  __shared__ float4 so[kGroups][kLanes];
-  const bool by_row = parts <= 8;
-  for (int r0 = blockIdx.y * 8; r0 < g.rows && r0 < (int)(blockIdx.y + 1) * 8; r0 += by_row ? kGroups : 1) {
-    const int rho = by_row ? r0 + group : r0;
-    const bool on = rho < g.rows && rho < (int)(blockIdx.y + 1) * 8;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on)
-      for (int i = by_row ? 0 : group; i < parts; i += by_row ? 1 : kGroups) {
-        const float* s = slot(i);
-        const float2 ml = *reinterpret_cast<const float2*>(s + (size_t)ROWS * D + 2 * rho);
-        const float4 x = *reinterpret_cast<const float4*>(s + (size_t)rho * D + d);
-        const float top = fmaxf(m, ml.x);
-        const float f0 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-        const float f1 = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-        // a part without visible keys has m = -inf, l = 0, O = 0; NaN parts have a NaN l
-        l = l * f0 + (ml.x == -INFINITY ? ml.y : ml.y * f1);
-        o.x = o.x * f0 + x.x * f1;
-        o.y = o.y * f0 + x.y * f1;
-        o.z = o.z * f0 + x.z * f1;
-        o.w = o.w * f0 + x.w * f1;
-        m = top;
-      }
-    if (!by_row) {
-      __syncthreads();
-      so[group][threadIdx.x % kLanes] = o;
-      if (d == 0) {
-        sm[group] = m;
-        sl[group] = l;
-      }
-      __syncthreads();
-      if (group != 0) continue;
-      for (int i = 1; i < kGroups; ++i) {
-        const float top = fmaxf(m, sm[i]);
-        const float f0 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-        const float f1 = sm[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[i] - top);
-        const float4 x = so[i][threadIdx.x % kLanes];
-        l = l * f0 + (sm[i] == -INFINITY ? sl[i] : sl[i] * f1);
-        o.x = o.x * f0 + x.x * f1;
-        o.y = o.y * f0 + x.y * f1;
-        o.z = o.z * f0 + x.z * f1;
-        o.w = o.w * f0 + x.w * f1;
-        m = top;
-      }
-    }
-    if (!on) continue;
+  auto weight = [](float m, float top) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
+  auto share = [](float m, float l, float f) { return m == -INFINITY ? l : l * f; };  // (such an l is 0 or NaN)
+  auto add = [](float4& o, const float4& x, float f) {
+    o.x = fmaf(x.x, f, o.x);
+    o.y = fmaf(x.y, f, o.y);
+    o.z = fmaf(x.z, f, o.z);
+    o.w = fmaf(x.w, f, o.w);
+  };
+  auto store = [&](int rho, float top, float l, float4 o) {
     int hq;
     const long long row = global_row(a, g, rho, rec.head, hq);
-    if (row < 0) continue;
+    if (row < 0) return;
     const float f = row_factor(l, vs);
     if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-    store4<CT>(a.out, row * a.out_stride + (size_t)hq * D + d, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
-    if (a.lse && d == 0) a.lse[row * a.c.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
+    store4<CT>(a.out, row * a.out_stride + (size_t)hq * D + 4 * lane, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+    if (a.lse && lane == 0) a.lse[row * a.c.Hq + hq] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2f;
+  };
+  if (parts <= kFewParts) {
+    for (int rho = blockIdx.y * kGroups + group; rho < g.rows; rho += kJoinY * kGroups) {
+      float top = -INFINITY, l = 0.f;
+      for (int i = 0; i < parts; ++i) top = fmaxf(top, slot(i)[(size_t)ROWS * D + 2 * rho]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < parts; ++i) {
+        const float* s = slot(i);
+        const float2 ml = *reinterpret_cast<const float2*>(s + (size_t)ROWS * D + 2 * rho);
+        const float f = weight(ml.x, top);
+        l += share(ml.x, ml.y, f);
+        add(o, *reinterpret_cast<const float4*>(s + (size_t)rho * D + 4 * lane), f);
+      }
+      store(rho, top, l, o);
+    }
+    return;
+  }
+  __shared__ float factor[2 * kCUs], sh[kAttendThreads / 64];
+  __shared__ float4 so[kGroups][kLanes];
+  for (int rho = blockIdx.y; rho < g.rows; rho += kJoinY) {
+    float2 ml[2];  // parts are at most the workers, two a thread
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = e * kAttendThreads + threadIdx.x;
+      ml[e] = i < parts ? *reinterpret_cast<const float2*>(slot(i) + (size_t)ROWS * D + 2 * rho)
+                        : make_float2(-INFINITY, 0.f);
+    }
+    float top = wave_max(fmaxf(ml[0].x, ml[1].x));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
+    float l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float f = weight(ml[e].x, top);
+      factor[e * kAttendThreads + threadIdx.x] = f;
+      l += share(ml[e].x, ml[e].y, f);
+    }
+    l = wave_sum(l);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = l;
+    __syncthreads();
+    l = sh[0] + sh[1] + sh[2] + sh[3];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = group; i0 < parts; i0 += 8 * kGroups) {
+      float4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        x[u] = *reinterpret_cast<const float4*>(slot(min(i0 + u * kGroups, parts - 1)) + (size_t)rho * D + 4 * lane);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * kGroups < parts) add(o, x[u], factor[i0 + u * kGroups]);
+    }
+    so[group][lane] = o;
+    __syncthreads();
+    if (group == 0) {
+      for (int i = 1; i < kGroups; ++i) add(o, so[i][lane], 1.f);
+      store(rho, top, l, o);
+    }
   }
 }
 

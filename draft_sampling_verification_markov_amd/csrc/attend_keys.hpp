@@ -84,8 +84,11 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
       }
       const Data* src = static_cast<const Data*>(a.q) + (r >= 0 ? r * a.q_stride + (size_t)hq * D : 0);
 #pragma unroll
+      for (int x = 0; x < kQ; ++x) q[nb][x] = *reinterpret_cast<const uint4*>(src + coord<CT>(x, h));
+      const uint32_t there = r >= 0 ? ~0u : 0u;
+#pragma unroll
       for (int x = 0; x < kQ; ++x)
-        q[nb][x] = r >= 0 ? *reinterpret_cast<const uint4*>(src + coord<CT>(x, h)) : make_uint4(0, 0, 0, 0);
+        q[nb][x] = make_uint4(q[nb][x].x & there, q[nb][x].y & there, q[nb][x].z & there, q[nb][x].w & there);
     }
     const float ks = CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2;
 
@@ -147,13 +150,20 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
       if (!full) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) mask_scores<kF32>(w[nb], row_lo[nb] - key0, row_hi[nb] - key0, h);
-        bool bad = false;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_)
+        for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_) {
+          const KeyMask<CT, typename TT::V> keep(key0 + (kF32 ? 8 * sl_ + 4 * h : 16 * sl_ + 8 * h), g.lo, g.hi);
 #pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db)
-            bad |= keep_keys<CT>(v[sl_][db], key0 + (kF32 ? 8 * sl_ + 4 * h : 16 * sl_ + 8 * h), g.lo, g.hi);
-        if (bad) odd = 1;
+          for (int db = 0; db < TT::kBlocks; ++db) keep.apply(v[sl_][db], bits);
+        }
+        if (__any(bits & KeyMask<CT, typename TT::V>::kOdd)) {
+          odd = 1;
+#pragma unroll
+          for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_)
+#pragma unroll
+            for (int db = 0; db < TT::kBlocks; ++db) v[sl_][db] = finite_part<CT>(v[sl_][db]);
+        }
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -189,7 +199,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
             so[wave][8 * db + 2 * j + h][col] = make_float4(acc[nb][db][4 * j] * f, acc[nb][db][4 * j + 1] * f,
                                                             acc[nb][db][4 * j + 2] * f, acc[nb][db][4 * j + 3] * f);
         __syncthreads();
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 32 * (D / 4) / kAttendThreads; ++i) {
           const int at = i * kAttendThreads + threadIdx.x, d4 = at % (D / 4), r = at / (D / 4), rho = nb * 32 + r;
           if (rho < g.rows) {

@@ -39,7 +39,7 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   k_attend_keys<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, NB * 32><<<dim3(pl.split.workers, NB * 4), kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, NB * 32><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
   return hipGetLastError();
 }
 

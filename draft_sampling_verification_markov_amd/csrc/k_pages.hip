@@ -7,6 +7,8 @@
 // or atomics run (sums of references, ranks from prefix sums, lowest free ids
 // first).  Device-wide dependencies are launch boundaries: a launch of the next
 // kernel costs about 2 us on the stream, a grid barrier over 8 XCDs no less.
+#include <type_traits>
+
 #include "dspark_cache_internal.hpp"
 
 namespace dspark {
@@ -37,23 +39,27 @@ struct CacheType<DSPARK_BF16> { using T = uint16_t; };
 template <>
 struct CacheType<DSPARK_F8E4M3> { using T = uint8_t; };
 
-// two stored elements of two data elements
+// two neighbouring data elements, and what the cache stores for them
 template <int CT>
-__device__ __forceinline__ void load_pair(const void* x, long long i, float scale, typename CacheType<CT>::T (&o)[2]) {
+struct DataPair {
+  using T = typename std::conditional<CT == DSPARK_F32, uint2, uint32_t>::type;
+  __device__ __forceinline__ static T load(const void* x, long long i) {
+    return *reinterpret_cast<const T*>(static_cast<const char*>(x) + i * (CT == DSPARK_F32 ? 4 : 2));
+  }
+};
+template <int CT>
+__device__ __forceinline__ void store_type(const typename DataPair<CT>::T& w, float scale,
+                                           typename CacheType<CT>::T (&o)[2]) {
   if constexpr (CT == DSPARK_F32) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint32_t*>(x) + i);
     o[0] = w.x;
     o[1] = w.y;
+  } else if constexpr (CT == DSPARK_BF16) {
+    o[0] = (uint16_t)w;
+    o[1] = (uint16_t)(w >> 16);
   } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x) + i);
-    if constexpr (CT == DSPARK_BF16) {
-      o[0] = (uint16_t)w;
-      o[1] = (uint16_t)(w >> 16);
-    } else {
-      const uint32_t p = f8_pair(bf16_lo(w) / scale, bf16_hi(w) / scale);
-      o[0] = (uint8_t)p;
-      o[1] = (uint8_t)(p >> 8);
-    }
+    const uint32_t p = f8_pair(bf16_lo(w) / scale, bf16_hi(w) / scale);
+    o[0] = (uint8_t)p;
+    o[1] = (uint8_t)(p >> 8);
   }
 }
 
@@ -79,17 +85,23 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int b, int gi)
   T* const vd = static_cast<T*>(a.v_pool) + (block + off) * D + (size_t)d * 8;
   const float ks = CT == DSPARK_F8E4M3 ? a.k_scale[head] : 1.f, vs = CT == DSPARK_F8E4M3 ? a.v_scale[head] : 1.f;
   const long long row0 = c.first_row(b) + (j0 - pos0);
-  T kx[8][2], vx[8][2];
+  // all loads at once: rows that are not there are read as the nearest one that is
+  typename DataPair<CT>::T kw[8], vw[8];
   bool has[8], all = true;
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    const long long r = row0 + t;
+    const long long r = row0 + t, near = row0 + min(max(t, lo - j0), hi - 1 - j0);
     has[t] = j0 + t >= lo && j0 + t < hi && c.has_row(r);
     all = all && has[t];
-    if (has[t]) {
-      load_pair<CT>(a.k, r * a.k_stride + head * D + d, ks, kx[t]);
-      load_pair<CT>(a.v, r * a.v_stride + head * D + d, vs, vx[t]);
-    }
+    const long long safe = near < 0 ? 0 : near < c.n_rows ? near : c.n_rows - 1;
+    kw[t] = DataPair<CT>::load(a.k, safe * a.k_stride + head * D + d);
+    vw[t] = DataPair<CT>::load(a.v, safe * a.v_stride + head * D + d);
+  }
+  T kx[8][2], vx[8][2];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    store_type<CT>(kw[t], ks, kx[t]);
+    store_type<CT>(vw[t], vs, vx[t]);
   }
 #pragma unroll
   for (int t = 0; t < 8; ++t)
@@ -235,17 +247,26 @@ __global__ __launch_bounds__(kThreads) void k_ref_move(PagesArgs a) {
 template <bool LIVE>
 __device__ __forceinline__ bool counts(int ref) { return LIVE ? ref > 0 : ref == 0; }
 
+// A thread's consecutive pages of a block: their references (-1 past the pool), all
+// loads in flight at once.
+constexpr int kPerThread = kPageBlock / kThreads;
+__device__ __forceinline__ void load_refs(const int32_t* ref, int n_pages, int block, int (&r)[kPerThread]) {
+  const int p0 = block * kPageBlock + threadIdx.x * kPerThread;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) r[i] = ref[min(p0 + i, n_pages - 1)];
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) r[i] = p0 + i < n_pages ? r[i] : -1;
+}
+
 template <bool LIVE>
 __global__ __launch_bounds__(kThreads) void k_count(PagesArgs a, const int32_t* ref, int blocks) {
   __shared__ int sh[kThreads / 64];
   if ((int)blockIdx.x < blocks) {
+    int r[kPerThread];
+    load_refs(ref, a.n_pages, blockIdx.x, r);
     int n = 0;
-    const int p0 = blockIdx.x * kPageBlock;
 #pragma unroll
-    for (int i = 0; i < kPageBlock; i += kThreads) {
-      const int p = p0 + i + threadIdx.x;
-      n += p < a.n_pages && counts<LIVE>(ref[p]);
-    }
+    for (int i = 0; i < kPerThread; ++i) n += counts<LIVE>(r[i]);
     n = block_sum(n, sh);
     if (threadIdx.x == 0) a.block_count[blockIdx.x] = n;
     return;
@@ -286,18 +307,19 @@ __device__ __forceinline__ int counted_before(const PagesArgs& a, int block, int
 // in that list.
 __global__ __launch_bounds__(kThreads) void k_free_list(PagesArgs a, int blocks) {
   __shared__ int sh[kThreads / 64];
+  int mine[kPerThread];
+  if ((int)blockIdx.x < blocks) load_refs(a.ref_out, a.n_pages, blockIdx.x, mine);
   int total;
   int at = counted_before(a, blockIdx.x, blocks, sh, total);
   if ((int)blockIdx.x < blocks) {
-    const int p0 = blockIdx.x * kPageBlock;
-    for (int i = 0; i < kPageBlock; i += kThreads) {
-      const int p = p0 + i + threadIdx.x;
-      const int free = p < a.n_pages && counts<false>(a.ref_out[p]);
-      int n;
-      const int r = block_prefix(free, sh, n);
-      if (free) a.ids[at + r] = p;
-      at += n;
-    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) n += counts<false>(mine[i]);
+    at += block_prefix(n, sh, n);
+    const int p0 = blockIdx.x * kPageBlock + threadIdx.x * kPerThread;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (counts<false>(mine[i])) a.ids[at++] = p0 + i;
     return;
   }
   long long base = 0;  // requests may ask for more pages than 31 bits count
@@ -345,33 +367,40 @@ __global__ __launch_bounds__(kThreads) void k_table(PagesArgs a) {
 // there are equally many.  `rank` of a source, `ids` the holes, `src` the sources.
 __global__ __launch_bounds__(kThreads) void k_compact_rank(PagesArgs a, int blocks) {
   __shared__ int sh[kThreads / 64];
+  int mine[kPerThread], edge_refs[kPerThread];
+  load_refs(a.ref, a.n_pages, blockIdx.x, mine);
   int n_live;
   int at = counted_before(a, blockIdx.x, blocks, sh, n_live);
   // live ids below n_live: the whole blocks before n_live's, and the part of it
   const int edge = n_live / kPageBlock;  // n_live < n_pages, or every page is live and below
   int unused, part = 0;
   const int whole = counted_before(a, edge, blocks, sh, unused);
-  for (int p = edge * kPageBlock + threadIdx.x; p < n_live; p += kThreads) part += a.ref[p] > 0;
+  load_refs(a.ref, a.n_pages, edge, edge_refs);
+  const int e0 = edge * kPageBlock + threadIdx.x * kPerThread;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) part += e0 + i < n_live && edge_refs[i] > 0;
   const int below = whole + block_sum(part, sh);
-  const int p0 = blockIdx.x * kPageBlock;
-  for (int i = 0; i < kPageBlock; i += kThreads) {
-    const int p = p0 + i + threadIdx.x;
-    const int ref = p < a.n_pages ? a.ref[p] : 0;
-    const int live = ref > 0;
-    int n;
-    const int before = at + block_prefix(live, sh, n);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) n += mine[i] > 0;
+  at += block_prefix(n, sh, n);  // live ids before this thread's first
+  const int p0 = blockIdx.x * kPageBlock + threadIdx.x * kPerThread;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int p = p0 + i, ref = mine[i];
+    const bool live = ref > 0;
     if (p < a.n_pages) {
       if (p >= n_live) {
         a.ref_out[p] = 0;
-        a.rank[p] = live ? before - below : -1;
-        if (live) a.src[before - below] = p;
+        a.rank[p] = live ? at - below : -1;
+        if (live) a.src[at - below] = p;
       } else if (live) {
         a.ref_out[p] = ref;
       } else {
-        a.ids[p - before] = p;
+        a.ids[p - at] = p;
       }
     }
-    at += n;
+    at += live;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *a.count = n_live;
