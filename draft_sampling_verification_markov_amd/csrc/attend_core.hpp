@@ -18,11 +18,10 @@
 //
 // What a row does not see must not reach it, not even as NaN times a weight of 0.
 // Scores are replaced before the exponential.  In the tiles that some rows see in part
-// or not at all (the sequence's end, the diagonal, a window's edge) the values of keys
-// that no row sees, and all that are not finite, are replaced by 0; if a row does see
-// one that is not, the coordinate's result is made NaN or infinite when it is stored
-// (add_nonfinite), from the values themselves.  All other tiles are seen whole by all
-// rows and need no such care.
+// or not at all (the sequence's end, the diagonal, a window's edge) values that are not
+// finite are replaced by 0; if a row does see one, the coordinate's result is made NaN
+// or infinite when it is stored (add_nonfinite), from the values themselves.  All other
+// tiles are seen whole by all rows and need no such care.
 #pragma once
 
 #include <type_traits>
@@ -39,10 +38,11 @@ constexpr int kAttendThreads = 256;
 constexpr float kRescale = 8.f;  // log2 of the weight up to which the maximum may lag
 constexpr int kCUs = 256;
 
-// How the work of a call is dealt out.  A segment is one (item, kv head), an item one
-// row tile of one request; a unit is `unit` keys of a segment.  With `workers` 0 every
-// workgroup takes one whole segment; else the units of all segments, in order, are
-// dealt evenly to the workers, whose first and last segments may be partial.
+// How the work of a call is dealt out.  A segment is one (request, kv head, row tile),
+// in that order, so that neighbours read the same keys; a unit is `unit` keys of a
+// segment.  With `workers` 0 every workgroup takes one whole segment; else the units of
+// all segments, in order, are dealt evenly to the workers, whose first and last
+// segments may be partial.
 struct Split {
   int row_tiles;  // of a request, at most
   int workers;
@@ -50,14 +50,15 @@ struct Split {
 };
 
 // A partial segment: O (unnormalised) [rows][D], then (m, l) [rows]; two a worker.
-struct Record {  // of a worker whose first unit lies inside a segment (item -1: it does not)
-  int item, head;
+struct Record {  // of a worker whose first unit lies inside a segment (b -1: it does not)
+  int b, head, row_tile;
   int first, last;  // workers that share the segment
   int slot;         // of the first one's part; the others' is twice their number
 };
 
 struct Geometry {
-  int b, row0, rows;      // request; first row of the tile among the request's; rows in it
+  int b, row_tile;
+  int row0, rows;         // first row of the tile among the request's; rows in it
   int n, pos0;            // new tokens; position of token 0
   int lo, hi;             // keys that some row sees
   int all_lo, all_hi;     // keys in [all_lo, all_hi) are seen by every row
@@ -71,11 +72,11 @@ struct Masks {
 };
 
 template <int ROWS>
-__device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int item) {
+__device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int b, int rt) {
   Geometry g;
   const int G = a.c.Hq / a.c.Hkv;
-  g.b = p.row_tiles == 1 ? item : item / p.row_tiles;
-  const int rt = p.row_tiles == 1 ? 0 : item % p.row_tiles;
+  g.b = b;
+  g.row_tile = rt;
   g.n = a.c.rows(g.b);
   const int len = a.c.len(g.b);
   g.pos0 = len - g.n;
@@ -98,75 +99,122 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p
 
 // Position in the dealt work: the segment that holds a worker's first unit.
 struct Start {
-  int item, head, skip;  // units of the segment before the worker's first
-  int count;             // the worker's units
-  int workers;           // that have any
+  int b, head, row_tile;
+  int skip;   // units of the segment before the worker's first
+  int count;  // the worker's units
+  int workers;  // that have any
   long long unit, total;
 };
 
-__device__ __forceinline__ int wg_sum(int v, int* sh) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+// Exclusive prefix over the workgroup's 256 threads; all receives the sum.
+__device__ __forceinline__ int wg_prefix(int v, int* sh, int& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  if (lane == 63) sh[wave] = x;
   __syncthreads();
-  return sh[0] + sh[1] + sh[2] + sh[3];
+  const int s0 = sh[0], s1 = sh[1], s2 = sh[2], s3 = sh[3];
+  all = s0 + s1 + s2 + s3;
+  return x - v + (wave > 0 ? s0 : 0) + (wave > 1 ? s1 : 0) + (wave > 2 ? s2 : 0);
 }
 
-// Every worker finds its own start: the units of all items are summed in chunks of
-// 256 (one item a thread), then the chunk that holds the start is searched.  For the
-// batches that are dealt (up to a few thousand items) that is cheaper than a launch
-// of its own.
+// Every worker finds its own start.  (Request, row tile) pairs are summed in chunks of
+// 256, one a thread; the request is the last one whose units begin at or before the
+// worker's, and within it the head and then the row tile follow.  For the batches that
+// are dealt (up to a few thousand pairs) that is cheaper than a launch of its own.
 template <int ROWS>
 __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p, int worker, int* sh) {
-  const int items = a.c.B * p.row_tiles;
-  __shared__ int found[2];
+  const int RT = p.row_tiles, Hkv = a.c.Hkv;
+  const long long pairs = (long long)a.c.B * RT;
+  __shared__ int found_b, found_rt, found_skip;
+  __shared__ long long found_before;
+  auto tiles_of = [&](long long i) {
+    return i < pairs ? geometry<ROWS>(a, p, RT == 1 ? (int)i : (int)(i / RT), RT == 1 ? 0 : (int)(i % RT)).tiles : 0;
+  };
+  Start s{};
   long long total = 0;
-  for (int c = 0; c < items; c += kAttendThreads) {
-    const int i = c + threadIdx.x;
-    total += wg_sum(i < items ? geometry<ROWS>(a, p, i).tiles : 0, sh);
+  int all, mine = 0;
+  for (long long c = 0; c < pairs; c += kAttendThreads) {
+    mine = tiles_of(c + threadIdx.x);
+    wg_prefix(mine, sh, all);
+    total += all;
   }
-  const int Hkv = a.c.Hkv;
-  Start s;
   s.total = total * Hkv;
   s.workers = (int)(s.total < p.workers ? s.total : p.workers);
-  s.unit = s.workers ? worker * s.total / s.workers : 0;
-  s.count = worker < s.workers ? (int)((worker + 1) * s.total / s.workers - s.unit) : 0;
-  s.item = s.head = s.skip = 0;
-  if (s.count == 0) return s;
+  if (worker >= s.workers) return s;
+  s.unit = worker * s.total / s.workers;
+  s.count = (int)((worker + 1) * s.total / s.workers - s.unit);
   long long before = 0;
-  for (int c = 0; c < items; c += kAttendThreads) {
-    const int i = c + threadIdx.x;
-    const int t = i < items ? geometry<ROWS>(a, p, i).tiles : 0;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int x = t;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(x, o);
-      if (lane >= o) x += y;
-    }
+  for (long long c = 0; c < pairs; c += kAttendThreads) {
+    const long long i = c + threadIdx.x;
+    if (pairs > kAttendThreads) mine = tiles_of(i);
+    const int ahead = wg_prefix(mine, sh, all);
+    // the last pair, if any, that opens a request with units at or before the worker's first
+    if (threadIdx.x == 0) found_rt = -1;
     __syncthreads();
-    if (lane == 63) sh[wave] = x;
+    const bool opens = i < pairs && (RT == 1 || i % RT == 0) && (before + ahead) * Hkv <= s.unit;
+    if (opens) atomicMax(&found_rt, (int)threadIdx.x);
     __syncthreads();
-    int base = 0, all = 0;
-    for (int w = 0; w < kAttendThreads / 64; ++w) {
-      if (w < wave) base += sh[w];
-      all += sh[w];
-    }
-    const long long u0 = (before + base + x - t) * Hkv;
-    if (s.unit < (before + all) * Hkv) {  // in this chunk
-      if (t > 0 && s.unit >= u0 && s.unit < u0 + (long long)t * Hkv) {
-        found[0] = i;
-        found[1] = (int)(s.unit - u0);
-      }
-      __syncthreads();
-      s.item = found[0];
-      const int tiles = geometry<ROWS>(a, p, s.item).tiles;
-      s.head = found[1] / tiles;
-      s.skip = found[1] % tiles;
-      return s;
+    if (opens && found_rt == (int)threadIdx.x) {
+      found_b = RT == 1 ? (int)i : (int)(i / RT);
+      found_before = before + ahead;
     }
     before += all;
+    __syncthreads();
+    if (before * Hkv > s.unit) break;
   }
+  s.b = found_b;
+  long long in = s.unit - found_before * Hkv;  // units into the request
+  if (RT == 1) {
+    const int t = geometry<ROWS>(a, p, s.b, 0).tiles;
+    s.head = (int)(in / t);
+    s.skip = (int)(in % t);
+    return s;
+  }
+  long long per_head = 0;
+  for (int c = 0; c < RT; c += kAttendThreads) {
+    mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
+    wg_prefix(mine, sh, all);
+    per_head += all;
+  }
+  s.head = (int)(in / per_head);
+  in %= per_head;
+  for (int c = 0; c < RT; c += kAttendThreads) {
+    if (RT > kAttendThreads) mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
+    const int ahead = wg_prefix(mine, sh, all);
+    if (mine > 0 && in >= ahead && in < ahead + mine) {
+      found_rt = c + threadIdx.x;
+      found_skip = (int)(in - ahead);
+    }
+    in -= all;
+    if (in < 0) break;
+  }
+  __syncthreads();
+  s.row_tile = found_rt;
+  s.skip = found_skip;
   return s;
+}
+
+// The next segment that has units (there is one).
+template <int ROWS>
+__device__ __forceinline__ Geometry next_segment(const AttendArgs& a, const Split& p, Start& s) {
+  s.skip = 0;
+  ++s.row_tile;
+  while (true) {
+    Geometry g;
+    if (s.row_tile < p.row_tiles && (g = geometry<ROWS>(a, p, s.b, s.row_tile)).tiles > 0) return g;
+    // the request's row tiles are done (or it has none): its next head, or the next request
+    if (s.row_tile > 0 && ++s.head < a.c.Hkv) {
+      s.row_tile = 0;
+      continue;
+    }
+    s.head = s.row_tile = 0;
+    ++s.b;
+  }
 }
 
 // A request's row of the page table, read over the scalar cache (uniform addresses).
@@ -336,40 +384,19 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
     return o;
   }
 }
-// Of a lane's 16 (8, e4m3) bytes of values, consecutive keys from key0 on: the bits of
-// the keys in [lo, hi).
+// kOdd bits are left in `odd` if an element of x is not finite: all exponent bits set
+// (e4m3: all bits but the sign), where adding one carries into the element's top bit.
+template <int CT>
+constexpr uint32_t kOdd = CT == DSPARK_F32 ? 0x80000000u : CT == DSPARK_BF16 ? 0x80008000u : 0x80808080u;
 template <int CT, typename V>
-struct KeyMask {
-  static constexpr int kWords = sizeof(V) / 4, kPer = CT == DSPARK_F32 ? 1 : CT == DSPARK_BF16 ? 2 : 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ KeyMask(int key0, int lo, int hi) {
+__device__ __forceinline__ void find_nonfinite(const V& x, uint32_t& odd) {
+  constexpr uint32_t kExp = CT == DSPARK_F32 ? 0x7F800000u : CT == DSPARK_BF16 ? 0x7F807F80u : 0x7F7F7F7Fu;
+  constexpr uint32_t kOne = CT == DSPARK_F32 ? 0x00800000u : CT == DSPARK_BF16 ? 0x00800080u : 0x01010101u;
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &x, sizeof(V));
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int key = key0 + i * kPer + e;
-        if (key >= lo && key < hi) w[i] |= kPer == 1 ? ~0u : ((1u << (32 / kPer & 31)) - 1) << (e * (32 / kPer));
-      }
-    }
-  }
-  // x without the other keys; kOdd bits are left in `odd` if an element is not finite
-  // (all exponent bits set, e4m3: all bits but the sign: adding one carries into the
-  // element's top bit)
-  static constexpr uint32_t kOdd = CT == DSPARK_F32 ? 0x80000000u : CT == DSPARK_BF16 ? 0x80008000u : 0x80808080u;
-  __device__ __forceinline__ void apply(V& x, uint32_t& odd) const {
-    constexpr uint32_t kExp = CT == DSPARK_F32 ? 0x7F800000u : CT == DSPARK_BF16 ? 0x7F807F80u : 0x7F7F7F7Fu;
-    constexpr uint32_t kOne = CT == DSPARK_F32 ? 0x00800000u : CT == DSPARK_BF16 ? 0x00800080u : 0x01010101u;
-    uint32_t y[kWords];
-    __builtin_memcpy(y, &x, sizeof(V));
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      y[i] &= w[i];
-      odd |= (y[i] & kExp) + kOne;
-    }
-    __builtin_memcpy(&x, y, sizeof(V));
-  }
-};
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i) odd |= (w[i] & kExp) + kOne;
+}
 template <int CT, typename V>
 __device__ __forceinline__ V finite_part(V x) {
   uint32_t w[sizeof(V) / 4];
@@ -378,6 +405,14 @@ __device__ __forceinline__ V finite_part(V x) {
   for (int i = 0; i < (int)(sizeof(V) / 4); ++i) w[i] = finite_word<CT>(w[i]);
   __builtin_memcpy(&x, w, sizeof(V));
   return x;
+}
+
+template <int CT, typename V>
+__device__ __forceinline__ bf16x8_t value_operand(const V& v) {
+  if constexpr (CT == DSPARK_BF16)
+    return as_bf16x8(v);
+  else
+    return f8_to_bf16x8(v.x, v.y);
 }
 
 // O^T += V^T P^T of one 32-row block
@@ -396,12 +431,7 @@ __device__ __forceinline__ void add_values(const typename Tile<CT, D>::V (&v)[Ti
     for (int s = 0; s < 2; ++s) {
       const bf16x8_t p = pack8(w, 8 * s);
 #pragma unroll
-      for (int db = 0; db < D / 32; ++db) {
-        if constexpr (CT == DSPARK_BF16)
-          acc[db] = mma(as_bf16x8(v[s][db]), p, acc[db]);
-        else
-          acc[db] = mma(f8_to_bf16x8(v[s][db].x, v[s][db].y), p, acc[db]);
-      }
+      for (int db = 0; db < D / 32; ++db) acc[db] = mma(value_operand<CT>(v[s][db]), p, acc[db]);
     }
   }
 }
@@ -410,6 +440,15 @@ __device__ __forceinline__ void add_values(const typename Tile<CT, D>::V (&v)[Ti
 // out and lse of one row from its sums
 __device__ __forceinline__ float row_factor(float l, float vs) { return l == 0.f ? 0.f : vs / l; }
 
+template <int CT>
+__device__ __forceinline__ float4 load4(const void* out, size_t at) {
+  if constexpr (CT == DSPARK_F32) {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(out) + at);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(out) + at);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  }
+}
 template <int CT>
 __device__ __forceinline__ void store4(void* out, size_t at, float4 y) {
   if constexpr (CT == DSPARK_F32) {
@@ -435,14 +474,16 @@ __device__ __forceinline__ float cached(const char* p) {
 }
 
 // What the values that are not finite make of coordinates d .. d + 3 of the row at
-// position pos: those of the keys in [k0, k1) outside [all_lo, all_hi) that it sees.
-template <int CT, int D>
+// position pos: those of the keys in [k0, k1) that it sees, in tiles of TILE keys that
+// are not wholly in [all_lo, all_hi) (the others' products took them as they are).
+template <int CT, int D, int TILE>
 __device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometry& g, const Masks& mask, int head,
                                               int pos, int d, int k0, int k1, float4& y) {
   const CacheView& c = a.c;
   const int lo = max(k0, mask.lo(pos)), hi = min(k1, mask.hi(pos));
   for (int key = lo; key < hi; ++key) {
-    if (key >= g.all_lo && key < g.all_hi) continue;
+    const int tile = key & ~(TILE - 1);
+    if (tile >= g.all_lo && tile + TILE <= g.all_hi) continue;
     const unsigned page = min((unsigned)c.table[(size_t)g.b * c.max_pages + (key >> c.page_shift)], (unsigned)c.n_pages - 1u);
     const size_t token = (((size_t)page * c.Hkv + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
     const char* src = static_cast<const char*>(a.v_pool) +
@@ -486,11 +527,12 @@ __device__ __forceinline__ Partials partials(const AttendArgs& a, const Split& p
 
 // Worker `worker`'s record (one thread writes it)
 __device__ __forceinline__ void put_record(const Partials& ws, const Start& s, int worker, int tiles) {
-  Record r{-1, 0, 0, 0, 0};
+  Record r{-1, 0, 0, 0, 0, 0};
   if (s.count > 0 && s.skip > 0) {
     const long long u0 = s.unit - s.skip;  // a unit u is worker ((u + 1) W - 1) / total's
-    r.item = s.item;
+    r.b = s.b;
     r.head = s.head;
+    r.row_tile = s.row_tile;
     r.first = (int)(((u0 + 1) * s.workers - 1) / s.total);
     r.last = (int)(((u0 + tiles) * s.workers - 1) / s.total);
     r.slot = 2 * r.first + (r.first * s.total / s.workers == u0 ? 0 : 1);
@@ -510,9 +552,9 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
   constexpr int kLanes = D / 4, kGroups = kAttendThreads / kLanes;  // a float4 a lane
   const Partials ws = partials(a, p);
   const Record rec = ws.records[blockIdx.x];
-  if (rec.item < 0 || (int)blockIdx.x != rec.first + 1) return;
+  if (rec.b < 0 || (int)blockIdx.x != rec.first + 1) return;
   const int parts = rec.last - rec.first + 1;
-  const Geometry g = geometry<ROWS>(a, p, rec.item);
+  const Geometry g = geometry<ROWS>(a, p, rec.b, rec.row_tile);
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
   auto slot = [&](int i) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };

@@ -37,22 +37,19 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
       return;
     }
   } else {
-    s.item = blockIdx.x / c.Hkv;
-    s.head = blockIdx.x % c.Hkv;
-    s.skip = 0;
+    s = Start{};
+    s.row_tile = blockIdx.x % p.row_tiles;
+    s.head = blockIdx.x / p.row_tiles % c.Hkv;
+    s.b = blockIdx.x / p.row_tiles / c.Hkv;
     s.count = 0x7fffffff;
   }
   int left = s.count;
   bool first_segment = true;
-  Geometry g = geometry<kRows>(a, p, s.item);
+  Geometry g = geometry<kRows>(a, p, s.b, s.row_tile);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
+  if (g.tiles == 0) return;  // a direct workgroup without rows
 
   while (true) {
-    if (g.tiles == 0) {  // no rows (dealt work has no units here; a direct workgroup is done)
-      if (!p.workers) return;
-      g = geometry<kRows>(a, p, ++s.item);
-      continue;
-    }
     const int t0 = g.tile0 + s.skip, take = min(left, g.tiles - s.skip), t1 = t0 + take;
     const int head = s.head, blocks = (g.rows + 31) >> 5;
 
@@ -152,12 +149,10 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
         for (int nb = 0; nb < NB; ++nb) mask_scores<kF32>(w[nb], row_lo[nb] - key0, row_hi[nb] - key0, h);
         uint32_t bits = 0;
 #pragma unroll
-        for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_) {
-          const KeyMask<CT, typename TT::V> keep(key0 + (kF32 ? 8 * sl_ + 4 * h : 16 * sl_ + 8 * h), g.lo, g.hi);
+        for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_)
 #pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db) keep.apply(v[sl_][db], bits);
-        }
-        if (__any(bits & KeyMask<CT, typename TT::V>::kOdd)) {
+          for (int db = 0; db < TT::kBlocks; ++db) find_nonfinite<CT>(v[sl_][db], bits);
+        if (__any(bits & kOdd<CT>)) {
           odd = 1;
 #pragma unroll
           for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_)
@@ -212,7 +207,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
                                    o0.w + o1.w + o2.w + o3.w);
             if (odd) {
               const int pos = g.pos0 + (g.row0 + rho) / G;
-              add_nonfinite<CT, D>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
+              add_nonfinite<CT, D, 32>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
             }
             if (whole) {
               int hq;
@@ -238,11 +233,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     left -= take;
     if (left <= 0) return;
     first_segment = false;
-    s.skip = 0;
-    if (++s.head == c.Hkv) {
-      s.head = 0;
-      g = geometry<kRows>(a, p, ++s.item);
-    }
+    g = next_segment<kRows>(a, p, s);
   }
 }
 

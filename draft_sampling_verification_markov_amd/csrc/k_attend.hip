@@ -2,6 +2,7 @@
 // kernel and split.  See include/dspark_cache.h for the contract, attend_core.hpp for
 // the mathematics.
 #include "attend_keys.hpp"
+#include "attend_rows.hpp"
 
 namespace dspark {
 namespace {
@@ -43,12 +44,32 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int CT, int D, int NB, int OCC>
+hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
+  constexpr int kRows = NB * 128;
+  const Plan pl = plan_for(C, a.c.max_new, a.window, kRows, RowsShape<CT, D, NB>::kKeys == 64 ? 6 : 5, OCC);
+  if (!pl.split.workers) {
+    k_attend_rows<CT, D, NB, OCC><<<C.B * pl.split.row_tiles * C.Hkv, kAttendThreads, 0, s>>>(a, pl.split);
+    return hipGetLastError();
+  }
+  k_attend_rows<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, kRows><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
+  return hipGetLastError();
+}
+
 template <int CT, int D>
 hipError_t run(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   const int rows = max_rows(C, a.c.max_new);
   constexpr int kOne = CT != DSPARK_F32 && D <= 128 ? 2 : 1;
-  if (rows <= 32 || D == 256) return run_keys<CT, D, 1, kOne>(C, a, s);
-  return run_keys<CT, D, D == 256 ? 1 : 2, 1>(C, a, s);
+  if (rows <= 32) return run_keys<CT, D, 1, kOne>(C, a, s);
+  if constexpr (CT == DSPARK_F32) {
+    return run_keys<CT, D, D == 256 ? 1 : 2, 1>(C, a, s);
+  } else if constexpr (D == 256) {
+    return run_rows<CT, D, 1, 1>(C, a, s);
+  } else {
+    if (rows <= 128) return run_rows<CT, D, 1, 2>(C, a, s);
+    return run_rows<CT, D, 2, 1>(C, a, s);
+  }
 }
 
 template <int CT>
@@ -59,8 +80,9 @@ hipError_t run_type(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new) {
-  // two partial results a worker, at most 64 rows and 2 workers a CU
-  return records_bytes(2 * kCUs) + (size_t)2 * 2 * kCUs * 64 * (C.D + 2) * sizeof(float);
+  // the records and two partial results a worker: 2 workers a CU with up to 128 rows, one with up to 256
+  const int rows = max_rows(C, max_new) <= 32 ? 32 : C.cache_dtype == DSPARK_F32 ? 64 : 128;
+  return records_bytes(2 * kCUs) + (size_t)2 * 2 * kCUs * rows * (C.D + 2) * sizeof(float);
 }
 
 hipError_t launch_cache_attend(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {

@@ -144,6 +144,20 @@ def test_attend_ignores_what_a_row_does_not_see(ds, dtype, bad, G):
         assert torch.isnan(out[0]).all() and torch.isnan(out[3:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "f8"])
+@pytest.mark.parametrize("G,rows", [(2, 6), (24, 6), (2, 40)])
+def test_attend_nan_that_every_row_sees(ds, dtype, G, rows):
+    # next to the diagonal, where some keys are hidden, and far from it
+    page, D = 16, 64
+    for j in (66, 3):
+        c = cu.make(5, dtype, page, D, G, 1, [rows], [70 + rows - 1])
+        p, off = c.table[0][j // page], j % page
+        c.v_pool[0, p, :, off // 8, 5, off % 8] = float("nan")
+        out, lse = gpu_attend(ds, c)
+        assert torch.isnan(out[:, :, 5]).all() and not torch.isnan(lse).any()
+        assert not torch.isnan(torch.cat([out[:, :, :5], out[:, :, 6:]], 2)).any()
+
+
 def test_attend_layers_strides_and_no_lse(ds):
     # the second of three layers; q and out are column slices of wider arrays
     page, D, Hq, Hkv = 16, 64, 4, 2
