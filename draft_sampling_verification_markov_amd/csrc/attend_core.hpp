@@ -106,7 +106,8 @@ struct Start {
   long long unit, total;
 };
 
-// Exclusive prefix over the workgroup's 256 threads; all receives the sum.
+// Exclusive prefix over the workgroup's THREADS threads; all receives the sum.
+template <int THREADS>
 __device__ __forceinline__ int wg_prefix(int v, int* sh, int& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int x = v;
@@ -117,30 +118,36 @@ __device__ __forceinline__ int wg_prefix(int v, int* sh, int& all) {
   __syncthreads();
   if (lane == 63) sh[wave] = x;
   __syncthreads();
-  const int s0 = sh[0], s1 = sh[1], s2 = sh[2], s3 = sh[3];
-  all = s0 + s1 + s2 + s3;
-  return x - v + (wave > 0 ? s0 : 0) + (wave > 1 ? s1 : 0) + (wave > 2 ? s2 : 0);
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    const int s = sh[w];
+    all += s;
+    before += w < wave ? s : 0;
+  }
+  return x - v + before;
 }
 
-// Every worker finds its own start.  (Request, row tile) pairs are summed in chunks of
-// 256, one a thread; the request is the last one whose units begin at or before the
+// Every worker finds its own start.  (Request, row tile) pairs are summed a
+// chunk at a time, one a thread; the request is the last one whose units begin at or before the
 // worker's, and within it the head and then the row tile follow.  For the batches that
 // are dealt (up to a few thousand pairs) that is cheaper than a launch of its own.
-template <int ROWS>
+template <int ROWS, int THREADS>
 __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p, int worker, int* sh) {
   const int RT = p.row_tiles, Hkv = a.c.Hkv;
   const long long pairs = (long long)a.c.B * RT;
   __shared__ int found_b, found_rt, found_skip;
   __shared__ long long found_before;
-  auto tiles_of = [&](long long i) {
+  auto tiles_of = [&](long long i) __attribute__((always_inline)) {
     return i < pairs ? geometry<ROWS>(a, p, RT == 1 ? (int)i : (int)(i / RT), RT == 1 ? 0 : (int)(i % RT)).tiles : 0;
   };
   Start s{};
   long long total = 0;
   int all, mine = 0;
-  for (long long c = 0; c < pairs; c += kAttendThreads) {
+  for (long long c = 0; c < pairs; c += THREADS) {
     mine = tiles_of(c + threadIdx.x);
-    wg_prefix(mine, sh, all);
+    wg_prefix<THREADS>(mine, sh, all);
     total += all;
   }
   s.total = total * Hkv;
@@ -149,10 +156,10 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   s.unit = worker * s.total / s.workers;
   s.count = (int)((worker + 1) * s.total / s.workers - s.unit);
   long long before = 0;
-  for (long long c = 0; c < pairs; c += kAttendThreads) {
+  for (long long c = 0; c < pairs; c += THREADS) {
     const long long i = c + threadIdx.x;
-    if (pairs > kAttendThreads) mine = tiles_of(i);
-    const int ahead = wg_prefix(mine, sh, all);
+    if (pairs > THREADS) mine = tiles_of(i);
+    const int ahead = wg_prefix<THREADS>(mine, sh, all);
     // the last pair, if any, that opens a request with units at or before the worker's first
     if (threadIdx.x == 0) found_rt = -1;
     __syncthreads();
@@ -176,16 +183,16 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
     return s;
   }
   long long per_head = 0;
-  for (int c = 0; c < RT; c += kAttendThreads) {
+  for (int c = 0; c < RT; c += THREADS) {
     mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
-    wg_prefix(mine, sh, all);
+    wg_prefix<THREADS>(mine, sh, all);
     per_head += all;
   }
   s.head = (int)(in / per_head);
   in %= per_head;
-  for (int c = 0; c < RT; c += kAttendThreads) {
-    if (RT > kAttendThreads) mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
-    const int ahead = wg_prefix(mine, sh, all);
+  for (int c = 0; c < RT; c += THREADS) {
+    if (RT > THREADS) mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
+    const int ahead = wg_prefix<THREADS>(mine, sh, all);
     if (mine > 0 && in >= ahead && in < ahead + mine) {
       found_rt = c + threadIdx.x;
       found_skip = (int)(in - ahead);
@@ -197,6 +204,25 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   s.row_tile = found_rt;
   s.skip = found_skip;
   return s;
+}
+
+// The segment of a workgroup that takes a whole one.  Workgroups go round the 8 XCDs;
+// a (request, head) pair's row tiles go to one XCD, next to each other, so that they
+// read the keys through one L2 at about the same time; the last ones, which see the
+// most keys, go first.
+__device__ __forceinline__ Start whole_segment(const AttendArgs& a, const Split& p) {
+  Start s{};
+  const unsigned slot = blockIdx.x >> 3;
+  const unsigned pair = (slot / p.row_tiles << 3) + (blockIdx.x & 7);
+  s.row_tile = p.row_tiles - 1 - (int)(slot % p.row_tiles);
+  s.head = (int)(pair % a.c.Hkv);
+  s.b = (int)(pair / a.c.Hkv);
+  s.count = 0x7fffffff;
+  return s;
+}
+// workgroups of such a launch: the pairs rounded up to whole rounds of the XCDs
+inline int whole_grid(const dspark_cache& C, const Split& p) {
+  return ((C.B * C.Hkv + 7) & ~7) * p.row_tiles;
 }
 
 // The next segment that has units (there is one).
@@ -321,30 +347,35 @@ struct Running {
   float m, l;
 };
 
-// Leaves the scores of the tile's keys that the row sees (lo <= key < hi).
+// Leaves the scores of the tile's keys that the row sees (lo <= key < hi).  The half's
+// offset goes into the bounds, so that a key is a constant.
 template <bool F32>
 __device__ __forceinline__ void mask_scores(f32x16_t& s, int lo, int hi, int h) {
+  const int from = lo - (F32 ? 4 : 8) * h;
+  const unsigned n = max(0, hi - lo);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int key = key_of_reg<F32>(i, h);
-    s[i] = key >= lo && key < hi ? s[i] : -INFINITY;
-  }
+  for (int i = 0; i < 16; ++i) s[i] = (unsigned)(key_of_reg<F32>(i, 0) - from) < n ? s[i] : -INFINITY;
 }
 
-// Weights of a tile from its scores; returns the factor by which O and l fade (1 for
-// most tiles).
-__device__ __forceinline__ float weights(f32x16_t& s, Running& r, float c) {
-  float top = s[0];
+// The running maximum over N score tiles of a row; returns the factor by which O and l
+// fade (1 for most tiles).
+template <int N>
+__device__ __forceinline__ float raise_max(const f32x16_t (&s)[N], Running& r, float c) {
+  float top = s[0][0];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
   top = halves32_max(top) * c;
-  float fade = 1.f;
-  if (__any(top > r.m + kRescale)) {
-    const float m = fmaxf(r.m, top);
-    fade = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
-    r.m = m;
-    r.l *= fade;
-  }
+  if (!__any(top > r.m + kRescale)) return 1.f;
+  const float m = fmaxf(r.m, top);
+  const float fade = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
+  r.m = m;
+  r.l *= fade;
+  return fade;
+}
+// Scores to weights; l grows by their sum.
+__device__ __forceinline__ void weights(f32x16_t& s, Running& r, float c) {
   const float ref = r.m == -INFINITY ? 0.f : r.m;
   float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
@@ -355,7 +386,6 @@ __device__ __forceinline__ float weights(f32x16_t& s, Running& r, float c) {
     sum1 += s[i + 1];
   }
   r.l += sum0 + sum1;
-  return fade;
 }
 
 __device__ __forceinline__ bf16x8_t pack8(const f32x16_t& s, int at) {
@@ -557,16 +587,16 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
   const Geometry g = geometry<ROWS>(a, p, rec.b, rec.row_tile);
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
-  auto slot = [&](int i) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };
-  auto weight = [](float m, float top) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
-  auto share = [](float m, float l, float f) { return m == -INFINITY ? l : l * f; };  // (such an l is 0 or NaN)
-  auto add = [](float4& o, const float4& x, float f) {
+  auto slot = [&](int i) __attribute__((always_inline)) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };
+  auto weight = [](float m, float top) __attribute__((always_inline)) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
+  auto share = [](float m, float l, float f) __attribute__((always_inline)) { return m == -INFINITY ? l : l * f; };  // (such an l is 0 or NaN)
+  auto add = [](float4& o, const float4& x, float f) __attribute__((always_inline)) {
     o.x = fmaf(x.x, f, o.x);
     o.y = fmaf(x.y, f, o.y);
     o.z = fmaf(x.z, f, o.z);
     o.w = fmaf(x.w, f, o.w);
   };
-  auto store = [&](int rho, float top, float l, float4 o) {
+  auto store = [&](int rho, float top, float l, float4 o) __attribute__((always_inline)) {
     int hq;
     const long long row = global_row(a, g, rho, rec.head, hq);
     if (row < 0) return;

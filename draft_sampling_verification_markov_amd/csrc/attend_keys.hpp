@@ -31,17 +31,14 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
   if (p.workers) {
     // neighbouring workers on one XCD (workgroups go round the 8 of them)
     worker = (blockIdx.x & 7) * (p.workers >> 3) + (blockIdx.x >> 3);
-    s = find_start<kRows>(a, p, worker, sh);
+    s = find_start<kRows, kAttendThreads>(a, p, worker, sh);
     if (s.count == 0) {
       if (threadIdx.x == 0) put_record(partials(a, p), s, worker, 0);
       return;
     }
   } else {
-    s = Start{};
-    s.row_tile = blockIdx.x % p.row_tiles;
-    s.head = blockIdx.x / p.row_tiles % c.Hkv;
-    s.b = blockIdx.x / p.row_tiles / c.Hkv;
-    s.count = 0x7fffffff;
+    s = whole_segment(a, p);
+    if (s.b >= c.B) return;
   }
   int left = s.count;
   bool first_segment = true;
@@ -102,11 +99,11 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     const char* const vp = static_cast<const char*>(a.v_pool);
     const TableRow row(c, g.b);
     struct Ids { int a, b; };  // of the tile's two halves of 16 keys
-    auto ids_of = [&](int key) { return Ids{row.raw(key), row.raw(key + 16)}; };
-    auto token = [&](int id, int key) {  // first byte of 16 consecutive tokens
+    auto ids_of = [&](int key) __attribute__((always_inline)) { return Ids{row.raw(key), row.raw(key + 16)}; };
+    auto token = [&](int id, int key) __attribute__((always_inline)) {  // first byte of 16 consecutive tokens
       return (((size_t)(row.id(id) * (unsigned)c.Hkv + head) << c.page_shift) + (key & off_mask)) * (D * kEs);
     };
-    auto load_k = [&](int key0_, Ids id, uint4(&k)[TT::kK]) {
+    auto load_k = [&](int key0_, Ids id, uint4(&k)[TT::kK]) __attribute__((always_inline)) {
       const size_t ta = token(id.a, key0_), tb = token(id.b, key0_ + 16);
       const int key = key_of_row<kF32>(col) & 15;
       const char* src = kp + (col < 16 ? ta : tb) + key * (D * kEs) + 16 * h;
@@ -163,11 +160,13 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
         if (nb < blocks) {
-          const float fade = weights(w[nb], run[nb], ks);
+          const f32x16_t(&one)[1] = reinterpret_cast<const f32x16_t(&)[1]>(w[nb]);
+          const float fade = raise_max(one, run[nb], ks);
           if (__any(fade != 1.f)) {
 #pragma unroll
             for (int db = 0; db < TT::kBlocks; ++db) acc[nb][db] *= fade;
           }
+          weights(w[nb], run[nb], ks);
           add_values<CT, D>(v, w[nb], acc[nb]);
         }
     }

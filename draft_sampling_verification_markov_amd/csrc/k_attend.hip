@@ -7,18 +7,20 @@
 namespace dspark {
 namespace {
 
-// Workgroups that the chip holds at once decide how many workers share the units.
 struct Plan {
   Split split;
-  int rows;     // of a tile
-  int slots;    // partial results
+  int rows;  // of a tile
 };
-
-constexpr int kDirectKeys = 1024;
 
 int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / C.Hkv); }
 
-Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int occupancy) {
+// Whole segments or dealt units, for a kernel of which the chip holds `slots` workgroups.
+// Whole segments need no partial results, and the row tiles of a head run side by side
+// through one L2; but they leave the chip idle where they are few or of unequal length.
+// Whole are: segments of few keys, where there is nothing to share out; and `whole` or
+// more times as many as the slots.
+constexpr int kFewKeys = 1024, kWholeKeys = 16, kWholeRows = 1;
+Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int slots, int whole) {
   Plan pl{};
   pl.rows = rows;
   pl.split.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
@@ -26,17 +28,16 @@ Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int 
   long long keys = (long long)C.max_pages * C.page;
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
   const long long segments = (long long)C.B * pl.split.row_tiles * C.Hkv;
-  // few keys a segment: nothing to share out
-  const bool direct = keys <= kDirectKeys && segments <= (1 << 22);
-  pl.split.workers = direct ? 0 : kCUs * occupancy;
+  const bool direct = segments <= (1 << 22) && (keys <= kFewKeys || segments >= (long long)whole * slots);
+  pl.split.workers = direct ? 0 : slots;
   return pl;
 }
 
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 32, 7, OCC);
+  const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 32, 7, OCC * kCUs, kWholeKeys);
   if (!pl.split.workers) {
-    k_attend_keys<CT, D, NB, OCC><<<C.B * pl.split.row_tiles * C.Hkv, kAttendThreads, 0, s>>>(a, pl.split);
+    k_attend_keys<CT, D, NB, OCC><<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
     return hipGetLastError();
   }
   k_attend_keys<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
@@ -44,16 +45,16 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int CT, int D, int NB, int OCC>
+template <int CT, int D>
 hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  constexpr int kRows = NB * 128;
-  const Plan pl = plan_for(C, a.c.max_new, a.window, kRows, RowsShape<CT, D, NB>::kKeys == 64 ? 6 : 5, OCC);
+  using S = RowsShape<CT, D>;
+  const Plan pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows);
   if (!pl.split.workers) {
-    k_attend_rows<CT, D, NB, OCC><<<C.B * pl.split.row_tiles * C.Hkv, kAttendThreads, 0, s>>>(a, pl.split);
+    k_attend_rows<CT, D><<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
     return hipGetLastError();
   }
-  k_attend_rows<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, kRows><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_rows<CT, D><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, S::kRows><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
   return hipGetLastError();
 }
 
@@ -62,14 +63,10 @@ hipError_t run(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   const int rows = max_rows(C, a.c.max_new);
   constexpr int kOne = CT != DSPARK_F32 && D <= 128 ? 2 : 1;
   if (rows <= 32) return run_keys<CT, D, 1, kOne>(C, a, s);
-  if constexpr (CT == DSPARK_F32) {
+  if constexpr (CT == DSPARK_F32)
     return run_keys<CT, D, D == 256 ? 1 : 2, 1>(C, a, s);
-  } else if constexpr (D == 256) {
-    return run_rows<CT, D, 1, 1>(C, a, s);
-  } else {
-    if (rows <= 128) return run_rows<CT, D, 1, 2>(C, a, s);
-    return run_rows<CT, D, 2, 1>(C, a, s);
-  }
+  else
+    return run_rows<CT, D>(C, a, s);
 }
 
 template <int CT>
@@ -80,7 +77,7 @@ hipError_t run_type(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new) {
-  // the records and two partial results a worker: 2 workers a CU with up to 128 rows, one with up to 256
+  // the records and two partial results a worker: at most 2 workers a CU, and tiles of 32, 64 or 128 rows
   const int rows = max_rows(C, max_new) <= 32 ? 32 : C.cache_dtype == DSPARK_F32 ? 64 : 128;
   return records_bytes(2 * kCUs) + (size_t)2 * 2 * kCUs * rows * (C.D + 2) * sizeof(float);
 }
