@@ -54,7 +54,7 @@ struct AppendArgs {
 hipError_t launch_cache_append(const dspark_cache& C, const AppendArgs& a, hipStream_t s);
 
 // Pages of one block of the free-page scan.
-constexpr int kPageBlock = 4096;
+constexpr int kPageBlock = 1024;
 inline int page_blocks(int n_pages) { return (n_pages + kPageBlock - 1) / kPageBlock; }
 
 struct PagesArgs {
