@@ -357,6 +357,15 @@ __device__ __forceinline__ void mask_scores(f32x16_t& s, int lo, int hi, int h) 
   for (int i = 0; i < 16; ++i) s[i] = (unsigned)(key_of_reg<F32>(i, 0) - from) < n ? s[i] : -INFINITY;
 }
 
+// The running maximum moves to include `top`; returns the factor by which O and l fade.
+__device__ __forceinline__ float fade_to(Running& r, float top) {
+  const float m = fmaxf(r.m, top);
+  const float fade = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
+  r.m = m;
+  r.l *= fade;
+  return fade;
+}
+
 // The running maximum over N score tiles of a row; returns the factor by which O and l
 // fade (1 for most tiles).
 template <int N>
@@ -368,11 +377,7 @@ __device__ __forceinline__ float raise_max(const f32x16_t (&s)[N], Running& r, f
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
   top = halves32_max(top) * c;
   if (!__any(top > r.m + kRescale)) return 1.f;
-  const float m = fmaxf(r.m, top);
-  const float fade = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
-  r.m = m;
-  r.l *= fade;
-  return fade;
+  return fade_to(r, top);
 }
 // Scores to weights; l grows by their sum.
 __device__ __forceinline__ void weights(f32x16_t& s, Running& r, float c) {
@@ -576,7 +581,7 @@ __device__ __forceinline__ void put_record(const Partials& ws, const Start& s, i
 // D / 4 threads takes a row, 8 rows a workgroup.  Many (a long context dealt to many
 // workers): the workgroup takes a row, its groups the parts in turn.
 constexpr int kJoinY = 8;
-constexpr int kFewParts = 8;
+constexpr int kFewParts = 8, kMaxParts = 4 * kCUs;  // (the most workers)
 template <int CT, int D, int ROWS>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Split p) {
   constexpr int kLanes = D / 4, kGroups = kAttendThreads / kLanes;  // a float4 a lane
@@ -621,24 +626,27 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
     }
     return;
   }
-  __shared__ float factor[2 * kCUs], sh[kAttendThreads / 64];
+  __shared__ float factor[kMaxParts], sh[kAttendThreads / 64];
   __shared__ float4 so[kGroups][kLanes];
   for (int rho = blockIdx.y; rho < g.rows; rho += kJoinY) {
-    float2 ml[2];  // parts are at most the workers, two a thread
+    float2 ml[kMaxParts / kAttendThreads];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kMaxParts / kAttendThreads; ++e) {
       const int i = e * kAttendThreads + threadIdx.x;
       ml[e] = i < parts ? *reinterpret_cast<const float2*>(slot(i) + (size_t)ROWS * D + 2 * rho)
                         : make_float2(-INFINITY, 0.f);
     }
-    float top = wave_max(fmaxf(ml[0].x, ml[1].x));
+    float top = ml[0].x;
+#pragma unroll
+    for (int e = 1; e < kMaxParts / kAttendThreads; ++e) top = fmaxf(top, ml[e].x);
+    top = wave_max(top);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
     float l = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kMaxParts / kAttendThreads; ++e) {
       const float f = weight(ml[e].x, top);
       factor[e * kAttendThreads + threadIdx.x] = f;
       l += share(ml[e].x, ml[e].y, f);

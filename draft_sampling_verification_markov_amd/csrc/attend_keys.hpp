@@ -1,28 +1,75 @@
 // Paged-cache attention for few rows: the four waves of a workgroup hold the same
-// rows (NB blocks of 32) and take turns over the keys, so that every key and value is
+// rows (NB blocks of 16) and take turns over the keys, so that every key and value is
 // loaded by one wave, straight into the registers that the matrix instructions read.
 //
-// Bound by HBM for a few rows (a decoding token of a group of 4 or 8 query heads, a
-// verification block): nothing is shared between waves, so LDS would only add a trip.
-// A wave keeps the next tile's keys and this tile's values in flight.  At a segment's
-// end the waves' sums meet in LDS.
+// Bound by HBM for a few rows (a decoding token of a group of 4 or 8 query heads):
+// nothing is shared between waves, so LDS would only add a trip.  A wave keeps the next
+// tile's keys and this tile's values in flight.  Blocks of 16 rows, not 32: half of the
+// registers of O and Q, so that more waves are in flight, and half of the softmax's
+// work on rows that are not there.  At a segment's end the waves' sums meet in LDS.
+//
+// Tiles of 32 keys are two S^T tiles of 16 keys x 16 rows.  With lane l = 16 g + c
+// (c < 16): S^T register (t, i) holds row (of Q) c, key row 4 g + i of S tile t.  The
+// bf16 product with the values takes 8 consecutive keys of each g, so K row m of tile t
+// is read from key 8 (m / 4) + 4 t + m % 4; the fp32 product takes one key of each g at
+// a time, and K row m of tile t is key 16 t + m.
 #pragma once
 
 #include "attend_core.hpp"
 
 namespace dspark {
 
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4_t mma16(bf16x8_t x, bf16x8_t y, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mma16(float x, float y, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0);
+}
+
+template <int CT, int D>
+struct KeysTile {
+  static constexpr bool kF32 = CT == DSPARK_F32;
+  static constexpr int kEs = Operand<CT>::kBytes;
+  static constexpr int kK = D * kEs / 64;  // 16-byte loads of a K row's part in a lane
+  static constexpr int kQ = kF32 ? D / 16 : D / 32;
+  static constexpr int kV = kF32 ? 2 : 1;  // loads of a lane's keys of one coordinate
+  static constexpr int kBlocks = D / 16;
+  using V = typename std::conditional<CT == DSPARK_F8E4M3, uint2, uint4>::type;
+  // first coordinate of Q register x in lane group g: where K's load has it
+  __device__ __forceinline__ static int coord(int x, int g) {
+    return kF32 ? 16 * x + 4 * g : CT == DSPARK_BF16 ? 32 * x + 8 * g : 64 * (x >> 1) + 16 * g + 8 * (x & 1);
+  }
+  __device__ __forceinline__ static int key_of_row(int t, int m) {
+    return kF32 ? 16 * t + m : 8 * (m >> 2) + 4 * t + (m & 3);
+  }
+  // key of S register (t, i) in lane group 0; group g adds group_keys * g
+  static constexpr int kGroupKeys = kF32 ? 4 : 8;
+  __device__ __forceinline__ static constexpr int key_of_reg(int t, int i) { return kF32 ? 16 * t + i : 4 * t + i; }
+};
+
+// The largest, or the sum, of the four lanes that hold a row.
+__device__ __forceinline__ float groups_max(float x) {
+  const float2 a = rows16(x);
+  return halves32_max(fmaxf(a.x, a.y));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+  const float2 a = rows16(x);
+  return halves32_sum(a.x + a.y);
+}
+
 template <int CT, int D, int NB, int OCC>
 __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs a, Split p) {
-  using TT = Tile<CT, D>;
+  using TT = KeysTile<CT, D>;
   constexpr bool kF32 = TT::kF32;
-  constexpr int kQ = q_regs<CT, D>(), kRows = NB * 32, kEs = Operand<CT>::kBytes;
+  constexpr int kRows = NB * 16, kEs = TT::kEs;
   using Data = typename Operand<CT>::Data;
   __shared__ int sh[4];
   __shared__ int odd;  // a value that is not finite was left out
-  __shared__ float sm[4][32], sl[4][32];
-  __shared__ float4 so[4][D / 4][32];
-  const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+  __shared__ float sm[4][16], sl[4][16];
+  __shared__ float4 so[4][D / 4][16];
+  const int lane = threadIdx.x & 63, col = lane & 15, g16 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const CacheView& c = a.c;
 
@@ -48,49 +95,12 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
 
   while (true) {
     const int t0 = g.tile0 + s.skip, take = min(left, g.tiles - s.skip), t1 = t0 + take;
-    const int head = s.head, blocks = (g.rows + 31) >> 5;
+    const int head = s.head, blocks = (g.rows + 15) >> 4;
 
-    // ---- rows
-    const Masks mask{a.causal, a.window, c.len(g.b)};
-    const int G = c.Hq / c.Hkv;
-    uint4 q[NB][kQ];
-    int row_lo[NB], row_hi[NB];
-    if (threadIdx.x == 0) odd = 0;
-    __syncthreads();
-    Running run[NB];
-    f32x16_t acc[NB][TT::kBlocks];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      run[nb].m = -INFINITY;
-      run[nb].l = 0.f;
-#pragma unroll
-      for (int db = 0; db < TT::kBlocks; ++db) acc[nb][db] = f32x16_t{};
-      const int rho = nb * 32 + col;
-      row_lo[nb] = 0;  // a column without a row sees everything and is left out at the end
-      row_hi[nb] = 0x7fffffff;
-      int hq;
-      long long r = -1;
-      if (rho < g.rows) {
-        r = global_row(a, g, rho, head, hq);
-        const int pos = g.pos0 + (g.row0 + rho) / G;
-        row_lo[nb] = mask.lo(pos);
-        row_hi[nb] = mask.hi(pos);
-      }
-      const Data* src = static_cast<const Data*>(a.q) + (r >= 0 ? r * a.q_stride + (size_t)hq * D : 0);
-#pragma unroll
-      for (int x = 0; x < kQ; ++x) q[nb][x] = *reinterpret_cast<const uint4*>(src + coord<CT>(x, h));
-      const uint32_t there = r >= 0 ? ~0u : 0u;
-#pragma unroll
-      for (int x = 0; x < kQ; ++x)
-        q[nb][x] = make_uint4(q[nb][x].x & there, q[nb][x].y & there, q[nb][x].z & there, q[nb][x].w & there);
-    }
-    const float ks = CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2;
-
-    // ---- keys
-    // This wave's tiles: every fourth one of the units that some row sees.  Page ids come
-    // over the scalar cache two tiles ahead, keys one tile ahead; past the last tile the
-    // last one is loaded again, so that the loop has no branch that would make the waits
-    // for its loads inexact.
+    // ---- keys: this wave's tiles, every fourth one of the units that some row sees.
+    // Page ids come over the scalar cache two tiles ahead, keys one tile ahead; past the
+    // last tile the last one is loaded again, so that the loop has no branch that would
+    // make the waits for its loads inexact.
     int key0 = (t0 << 7) + 32 * wave, last = ((t1 - 1) << 7) + 32 * wave;
     if (key0 + 32 <= g.lo) key0 += 128;
     while (last >= g.hi && last >= key0) last -= 128;
@@ -103,71 +113,171 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     auto token = [&](int id, int key) __attribute__((always_inline)) {  // first byte of 16 consecutive tokens
       return (((size_t)(row.id(id) * (unsigned)c.Hkv + head) << c.page_shift) + (key & off_mask)) * (D * kEs);
     };
-    auto load_k = [&](int key0_, Ids id, uint4(&k)[TT::kK]) __attribute__((always_inline)) {
-      const size_t ta = token(id.a, key0_), tb = token(id.b, key0_ + 16);
-      const int key = key_of_row<kF32>(col) & 15;
-      const char* src = kp + (col < 16 ? ta : tb) + key * (D * kEs) + 16 * h;
+    auto load_k = [&](int key0_, Ids id, uint4(&k)[2][TT::kK]) __attribute__((always_inline)) {
+      const size_t half[2] = {token(id.a, key0_), token(id.b, key0_ + 16)};
 #pragma unroll
-      for (int x = 0; x < TT::kK; ++x) k[x] = *reinterpret_cast<const uint4*>(src + 32 * x);
+      for (int t = 0; t < 2; ++t) {
+        const int key = TT::key_of_row(t, col);
+        const char* src = kp + (kF32 ? half[t] : (col < 8 ? half[0] : half[1])) + (key & 15) * (D * kEs) + 16 * g16;
+#pragma unroll
+        for (int x = 0; x < TT::kK; ++x) k[t][x] = *reinterpret_cast<const uint4*>(src + 64 * x);
+      }
     };
-    uint4 k[TT::kK];
+    uint4 k[2][TT::kK];
     Ids id0{}, id1{};
     if (key0 <= last) {
       id0 = ids_of(key0);
       id1 = ids_of(min(key0 + 128, last));
       load_k(key0, id0, k);
     }
+
+    // ---- rows
+    const Masks mask{a.causal, a.window, c.len(g.b)};
+    const int G = c.Hq / c.Hkv;
+    uint4 q[NB][TT::kQ];
+    int row_lo[NB], row_hi[NB];
+    if (threadIdx.x == 0) odd = 0;
+    Running run[NB];
+    f32x4_t acc[NB][TT::kBlocks];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      run[nb].m = -INFINITY;
+      run[nb].l = 0.f;
+#pragma unroll
+      for (int db = 0; db < TT::kBlocks; ++db) acc[nb][db] = f32x4_t{};
+      const int rho = nb * 16 + col;
+      row_lo[nb] = 0;  // a column without a row sees everything and is left out at the end
+      row_hi[nb] = 0x7fffffff;
+      int hq = 0;
+      long long r = -1;
+      if (rho < g.rows) {
+        r = global_row(a, g, rho, head, hq);
+        const int pos = g.pos0 + (g.row0 + rho) / G;
+        row_lo[nb] = mask.lo(pos);
+        row_hi[nb] = mask.hi(pos);
+      }
+      const Data* src = static_cast<const Data*>(a.q) + (r >= 0 ? r * a.q_stride + (size_t)hq * D : 0);
+#pragma unroll
+      for (int x = 0; x < TT::kQ; ++x) q[nb][x] = *reinterpret_cast<const uint4*>(src + TT::coord(x, g16));
+      const uint32_t there = r >= 0 ? ~0u : 0u;
+#pragma unroll
+      for (int x = 0; x < TT::kQ; ++x)
+        q[nb][x] = make_uint4(q[nb][x].x & there, q[nb][x].y & there, q[nb][x].z & there, q[nb][x].w & there);
+    }
+    const float ks = CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2;
+    __syncthreads();
+
     for (; key0 <= last; key0 += 128) {
       const int next = min(key0 + 128, last);
       const Ids id2 = ids_of(min(key0 + 256, last));
-      typename TT::V v[TT::kSlabs][TT::kBlocks];
+      typename TT::V v[TT::kV][TT::kBlocks];
       {
-        const size_t tok[2] = {token(id0.a, key0), token(id0.b, key0 + 16)};
+        // bf16, e4m3: the lane's 8 keys are group g16 of the tile; fp32: of S tile t, group
+        // 2 t + g16 / 2, the half g16 % 2
+        const size_t half[2] = {token(id0.a, key0), token(id0.b, key0 + 16)};
 #pragma unroll
-        for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_) {
-          // fp32: slab j is the 8-token group j, half h its tokens 4 h ..; else slab s has the groups 2 s + h
-          const char* src = kF32 ? vp + tok[sl_ >> 1] + ((sl_ & 1) * D + col) * 32 + 16 * h
-                                 : vp + tok[sl_] + (h * D + col) * (8 * kEs);
+        for (int t = 0; t < TT::kV; ++t) {
+          const char* src = kF32 ? vp + half[t] + ((g16 >> 1) * D + col) * 32 + 16 * (g16 & 1)
+                                 : vp + (g16 < 2 ? half[0] : half[1]) + ((g16 & 1) * D + col) * (8 * kEs);
 #pragma unroll
           for (int db = 0; db < TT::kBlocks; ++db)
-            v[sl_][db] = *reinterpret_cast<const typename TT::V*>(src + db * (32 * 8 * kEs));
+            v[t][db] = *reinterpret_cast<const typename TT::V*>(src + db * (16 * 8 * kEs));
         }
       }
-      f32x16_t w[NB];
+      f32x4_t w[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        w[nb] = nb < blocks ? scores<CT, D>(k, q[nb]) : f32x16_t{};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          w[nb][t] = f32x4_t{};
+          if (nb < blocks) {
+#pragma unroll
+            for (int x = 0; x < TT::kK; ++x) {
+              if constexpr (kF32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[nb][t] = mma16(lane4(k[t][x], e), lane4(q[nb][x], e), w[nb][t]);
+              } else if constexpr (CT == DSPARK_BF16) {
+                w[nb][t] = mma16(as_bf16x8(k[t][x]), as_bf16x8(q[nb][x]), w[nb][t]);
+              } else {
+                w[nb][t] = mma16(f8_to_bf16x8(k[t][x].x, k[t][x].y), as_bf16x8(q[nb][2 * x]), w[nb][t]);
+                w[nb][t] = mma16(f8_to_bf16x8(k[t][x].z, k[t][x].w), as_bf16x8(q[nb][2 * x + 1]), w[nb][t]);
+              }
+            }
+          }
+        }
       load_k(next, id1, k);
       id0 = id1;
       id1 = id2;
-      const bool full = key0 >= g.all_lo && key0 + 32 <= g.all_hi;
-      if (!full) {
+      if (key0 < g.all_lo || key0 + 32 > g.all_hi) {  // not every row sees the whole tile
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mask_scores<kF32>(w[nb], row_lo[nb] - key0, row_hi[nb] - key0, h);
+        for (int nb = 0; nb < NB; ++nb) {
+          const int from = row_lo[nb] - key0 - TT::kGroupKeys * g16;
+          const unsigned n = max(0, row_hi[nb] - row_lo[nb]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[nb][t][i] = (unsigned)(TT::key_of_reg(t, i) - from) < n ? w[nb][t][i] : -INFINITY;
+        }
         uint32_t bits = 0;
 #pragma unroll
-        for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_)
+        for (int t = 0; t < TT::kV; ++t)
 #pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db) find_nonfinite<CT>(v[sl_][db], bits);
+          for (int db = 0; db < TT::kBlocks; ++db) find_nonfinite<CT>(v[t][db], bits);
         if (__any(bits & kOdd<CT>)) {
           odd = 1;
 #pragma unroll
-          for (int sl_ = 0; sl_ < TT::kSlabs; ++sl_)
+          for (int t = 0; t < TT::kV; ++t)
 #pragma unroll
-            for (int db = 0; db < TT::kBlocks; ++db) v[sl_][db] = finite_part<CT>(v[sl_][db]);
+            for (int db = 0; db < TT::kBlocks; ++db) v[t][db] = finite_part<CT>(v[t][db]);
         }
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
         if (nb < blocks) {
-          const f32x16_t(&one)[1] = reinterpret_cast<const f32x16_t(&)[1]>(w[nb]);
-          const float fade = raise_max(one, run[nb], ks);
-          if (__any(fade != 1.f)) {
+          float top = w[nb][0][0];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, w[nb][t][i]);
+          top = groups_max(top) * ks;
+          if (__any(top > run[nb].m + kRescale)) {
+            const float fade = fade_to(run[nb], top);
 #pragma unroll
             for (int db = 0; db < TT::kBlocks; ++db) acc[nb][db] *= fade;
           }
-          weights(w[nb], run[nb], ks);
-          add_values<CT, D>(v, w[nb], acc[nb]);
+          const float ref = run[nb].m == -INFINITY ? 0.f : run[nb].m;
+          float sum = 0.f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[nb][t][i] = __builtin_amdgcn_exp2f(fmaf(w[nb][t][i], ks, -ref));
+              sum += w[nb][t][i];
+            }
+          run[nb].l += sum;
+          if constexpr (kF32) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int db = 0; db < TT::kBlocks; ++db)
+                  acc[nb][db] = mma16(lane4(v[t][db], e), w[nb][t][e], acc[nb][db]);
+          } else {
+            bf16x8_t pw;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                const bf16x2_t x = __builtin_convertvector(f32x2_t{w[nb][t][i], w[nb][t][i + 1]}, bf16x2_t);
+                pw[4 * t + i] = x[0];
+                pw[4 * t + i + 1] = x[1];
+              }
+#pragma unroll
+            for (int db = 0; db < TT::kBlocks; ++db)
+              acc[nb][db] = mma16(value_operand<CT>(v[0][db]), pw, acc[nb][db]);
+          }
         }
     }
 
@@ -178,8 +288,8 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
       if (nb < blocks) {
-        const float l = halves32_sum(run[nb].l);
-        if (h == 0) {
+        const float l = groups_sum(run[nb].l);
+        if (g16 == 0) {
           sm[wave][col] = run[nb].m;
           sl[wave][col] = l;
         }
@@ -188,40 +298,38 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
         const float f = run[nb].m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(run[nb].m - m);
 #pragma unroll
         for (int db = 0; db < TT::kBlocks; ++db)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            so[wave][8 * db + 2 * j + h][col] = make_float4(acc[nb][db][4 * j] * f, acc[nb][db][4 * j + 1] * f,
-                                                            acc[nb][db][4 * j + 2] * f, acc[nb][db][4 * j + 3] * f);
+          so[wave][4 * db + g16][col] = make_float4(acc[nb][db][0] * f, acc[nb][db][1] * f, acc[nb][db][2] * f,
+                                                    acc[nb][db][3] * f);
         __syncthreads();
 #pragma unroll 1
-        for (int i = 0; i < 32 * (D / 4) / kAttendThreads; ++i) {
-          const int at = i * kAttendThreads + threadIdx.x, d4 = at % (D / 4), r = at / (D / 4), rho = nb * 32 + r;
-          if (rho < g.rows) {
-            float top = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r])), sum = 0.f;
+        for (int at = threadIdx.x; at < 16 * (D / 4); at += kAttendThreads) {
+          const int d4 = at % (D / 4), r = at / (D / 4), rho = nb * 16 + r;
+          if (rho >= g.rows) break;
+          const float top = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+          float sum = 0.f;
 #pragma unroll
-            for (int w4 = 0; w4 < 4; ++w4)
-              sum += sm[w4][r] == -INFINITY ? sl[w4][r] : sl[w4][r] * __builtin_amdgcn_exp2f(sm[w4][r] - top);
-            const float4 o0 = so[0][d4][r], o1 = so[1][d4][r], o2 = so[2][d4][r], o3 = so[3][d4][r];
-            float4 y = make_float4(o0.x + o1.x + o2.x + o3.x, o0.y + o1.y + o2.y + o3.y, o0.z + o1.z + o2.z + o3.z,
-                                   o0.w + o1.w + o2.w + o3.w);
-            if (odd) {
-              const int pos = g.pos0 + (g.row0 + rho) / G;
-              add_nonfinite<CT, D, 32>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
+          for (int w4 = 0; w4 < 4; ++w4)
+            sum += sm[w4][r] == -INFINITY ? sl[w4][r] : sl[w4][r] * __builtin_amdgcn_exp2f(sm[w4][r] - top);
+          const float4 o0 = so[0][d4][r], o1 = so[1][d4][r], o2 = so[2][d4][r], o3 = so[3][d4][r];
+          float4 y = make_float4(o0.x + o1.x + o2.x + o3.x, o0.y + o1.y + o2.y + o3.y, o0.z + o1.z + o2.z + o3.z,
+                                 o0.w + o1.w + o2.w + o3.w);
+          if (odd) {
+            const int pos = g.pos0 + (g.row0 + rho) / G;
+            add_nonfinite<CT, D, 32>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
+          }
+          if (whole) {
+            int hq;
+            const long long to = global_row(a, g, rho, head, hq);
+            if (to >= 0) {
+              const float fr = row_factor(sum, vs);
+              if (sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
+              store4<CT>(a.out, to * a.out_stride + (size_t)hq * D + 4 * d4,
+                         make_float4(y.x * fr, y.y * fr, y.z * fr, y.w * fr));
+              if (a.lse && d4 == 0) a.lse[to * c.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
             }
-            if (whole) {
-              int hq;
-              const long long row = global_row(a, g, rho, head, hq);
-              if (row >= 0) {
-                const float fr = row_factor(sum, vs);
-                if (sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
-                store4<CT>(a.out, row * a.out_stride + (size_t)hq * D + 4 * d4,
-                           make_float4(y.x * fr, y.y * fr, y.z * fr, y.w * fr));
-                if (a.lse && d4 == 0) a.lse[row * c.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
-              }
-            } else {
-              *reinterpret_cast<float4*>(slot + (size_t)rho * D + 4 * d4) = y;
-              if (d4 == 0) *reinterpret_cast<float2*>(slot + (size_t)kRows * D + 2 * rho) = make_float2(top, sum);
-            }
+          } else {
+            *reinterpret_cast<float4*>(slot + (size_t)rho * D + 4 * d4) = y;
+            if (d4 == 0) *reinterpret_cast<float2*>(slot + (size_t)kRows * D + 2 * rho) = make_float2(top, sum);
           }
         }
         __syncthreads();

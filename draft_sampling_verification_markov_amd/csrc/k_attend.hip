@@ -35,13 +35,13 @@ Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int 
 
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 32, 7, OCC * kCUs, kWholeKeys);
+  const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys);
   if (!pl.split.workers) {
     k_attend_keys<CT, D, NB, OCC><<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
     return hipGetLastError();
   }
   k_attend_keys<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, NB * 32><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, NB * 16><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
   return hipGetLastError();
 }
 
@@ -58,13 +58,20 @@ hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Workgroups of k_attend_keys that a CU holds, by their registers.
+template <int CT, int D, int NB>
+constexpr int keys_per_cu() {
+  constexpr int kWidth = D / 64 * NB * (CT == DSPARK_F32 ? 2 : 1);
+  return kWidth <= 1 ? 4 : kWidth <= 2 ? 3 : kWidth <= 4 ? 2 : 1;
+}
+
 template <int CT, int D>
 hipError_t run(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   const int rows = max_rows(C, a.c.max_new);
-  constexpr int kOne = CT != DSPARK_F32 && D <= 128 ? 2 : 1;
-  if (rows <= 32) return run_keys<CT, D, 1, kOne>(C, a, s);
+  if (rows <= 16) return run_keys<CT, D, 1, keys_per_cu<CT, D, 1>()>(C, a, s);
+  // fp32 products take 16 times as long as bf16 ones: no kernel that shares loads is needed
   if constexpr (CT == DSPARK_F32)
-    return run_keys<CT, D, D == 256 ? 1 : 2, 1>(C, a, s);
+    return run_keys<CT, D, 256 / D, keys_per_cu<CT, D, 256 / D>()>(C, a, s);
   else
     return run_rows<CT, D>(C, a, s);
 }
@@ -77,9 +84,10 @@ hipError_t run_type(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new) {
-  // the records and two partial results a worker: at most 2 workers a CU, and tiles of 32, 64 or 128 rows
-  const int rows = max_rows(C, max_new) <= 32 ? 32 : C.cache_dtype == DSPARK_F32 ? 64 : 128;
-  return records_bytes(2 * kCUs) + (size_t)2 * 2 * kCUs * rows * (C.D + 2) * sizeof(float);
+  // the records and two partial results a worker: at most 4 workers a CU with tiles of 16 rows, 2 with 128
+  const bool few = max_rows(C, max_new) <= 16;
+  const int workers = (few ? 4 : 2) * kCUs, rows = few ? 16 : C.cache_dtype == DSPARK_F32 ? 64 : 128;
+  return records_bytes(workers) + (size_t)2 * workers * rows * (C.D + 2) * sizeof(float);
 }
 
 hipError_t launch_cache_attend(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {

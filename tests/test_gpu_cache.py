@@ -77,9 +77,11 @@ def test_attend_ragged(ds, dtype, D, Hq, Hkv, page):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "f8"])
-@pytest.mark.parametrize("causal,window", [(True, 1), (True, 16), (True, 33), (False, 0), (False, 7)])
-def test_attend_masks(ds, dtype, causal, window):
-    c = cu.make(2, dtype, 32, 128, 4, 2, [9, 1, 17], [100, 260, 17])
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 16), (True, 33), (False, 0), (False, 7), (True, 2000)])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("G", [2, 8])
+def test_attend_masks(ds, dtype, causal, window, wide, G):
+    c = cu.make(2, dtype, 32, 128, 2 * G, 2, [9, 1, 17, 0], [100, 260, 17, 40], width=200 if wide else None)
     check_attend(c, *gpu_attend(ds, c, causal=causal, window=window), cu.oracle_attend(c, causal=causal, window=window))
 
 
@@ -106,9 +108,12 @@ def test_attend_every_length(ds, dtype, n):
 @pytest.mark.parametrize("dtype,D,page", [("bf16", 128, 16), ("bf16", 128, 64), ("f8", 128, 128), ("f32", 64, 32),
                                           ("bf16", 256, 16), ("f8", 256, 32), ("f32", 256, 16), ("f32", 128, 64)])
 @pytest.mark.parametrize("rows,G", [(1, 3), (17, 4), (40, 2), (150, 2), (301, 1)])
-def test_attend_row_counts(ds, dtype, D, page, rows, G):
-    # every arrangement of rows: a few, some row blocks, several row tiles, over contexts that need several key tiles
-    c = cu.make(20 + rows, dtype, page, D, 2 * G, 2, [rows, 1, rows // 2], [rows + 333, 700, rows // 2])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_row_counts(ds, dtype, D, page, rows, G, wide):
+    # every arrangement of rows: a few, some row blocks, several row tiles, over contexts that need several key tiles;
+    # with a wide page table the keys are dealt out over the chip and joined
+    c = cu.make(20 + rows, dtype, page, D, 2 * G, 2, [rows, 1, rows // 2], [rows + 333, 700, rows // 2],
+                width=5000 // page if wide else None)
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
 
 
@@ -147,10 +152,10 @@ def test_attend_ignores_what_a_row_does_not_see(ds, dtype, bad, G):
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "f8"])
 @pytest.mark.parametrize("G,rows", [(2, 6), (24, 6), (2, 40)])
 def test_attend_nan_that_every_row_sees(ds, dtype, G, rows):
-    # next to the diagonal, where some keys are hidden, and far from it
+    # next to the diagonal, where some keys are hidden, and far from it; keys in one part and dealt out
     page, D = 16, 64
-    for j in (66, 3):
-        c = cu.make(5, dtype, page, D, G, 1, [rows], [70 + rows - 1])
+    for j, width in ((66, None), (3, None), (66, 100), (3, 100)):
+        c = cu.make(5, dtype, page, D, G, 1, [rows], [70 + rows - 1], width=width)
         p, off = c.table[0][j // page], j % page
         c.v_pool[0, p, :, off // 8, 5, off % 8] = float("nan")
         out, lse = gpu_attend(ds, c)
@@ -398,8 +403,8 @@ def test_cycle_of_cache_calls_matches_the_oracle(ds):
     p.v.fill_(float("nan"))
     rng = np.random.default_rng(8)
     T = 9
-    p.ws = torch.empty(ds.cache_workspace_bytes(p.C, T), dtype=torch.uint8, device="cuda")
     C = ds.Cache.make(B, 60, page, width, layers, Hq, Hkv, D)
+    p.ws = torch.empty(ds.cache_workspace_bytes(C, T), dtype=torch.uint8, device="cuda")
     keys = [np.zeros((layers, 0, Hkv, D)) for _ in range(B)]
     for cycle in range(7):
         n = rng.integers(0 if cycle else 1, T + 1, B)
