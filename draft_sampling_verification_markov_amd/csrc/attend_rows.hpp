@@ -42,9 +42,11 @@ __device__ __forceinline__ void schedule() {
   __builtin_amdgcn_sched_group_barrier(KIND, N, 0);
 }
 
-// 64 lanes x 16 bytes from each lane's own address to 1 KB of LDS, in lane order
-__device__ __forceinline__ void dma_1k(const char* src, unsigned char* lds) {
-  __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// 64 lanes x 16 bytes at the lanes' offsets + AT of the buffer to the 1 KB of LDS at AT, in
+// lane order (the instruction's offset counts on both sides)
+template <int AT>
+__device__ __forceinline__ void dma_1k(__amdgpu_buffer_rsrc_t src, int offset, unsigned char* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, offset, 0, AT, 0);
 }
 
 template <int CT, int D>
@@ -139,21 +141,24 @@ __global__ __launch_bounds__(kAttendThreads, 1) void k_attend_rows(AttendArgs a,
     }
     const float ks = CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2;
 
-    // the tile's first byte of the 16 keys that this wave brings
+    // the 16 keys (or values) of tile t that this wave brings, as a buffer
     auto source = [&](const void* pool, int raw, int t) __attribute__((always_inline)) {
-      const int key = t * S::kKeys + 16 * sub16;
+      const int key = min(t, t1 - 1) * S::kKeys + 16 * sub16;
       const size_t token = ((size_t)(row.id(raw) * (unsigned)c.Hkv + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
-      return static_cast<const char*>(pool) + token * (D * kEs);
+      return make_rsrc(static_cast<const char*>(pool) + token * (D * kEs), 16 * D * kEs);
     };
     auto dma_k = [&](int raw, int t, unsigned char* to) __attribute__((always_inline)) {
-      const char* const src = source(a.k_pool, raw, t);
+      const __amdgpu_buffer_rsrc_t src = source(a.k_pool, raw, t);
 #pragma unroll
-      for (int i = 0; i < kOps; ++i) dma_1k(src + k_src[i], to + (wave * kOps + i) * 1024);
+      for (int i = 0; i < kOps; ++i) dma_1k<0>(src, k_src[i], to + (wave * kOps + i) * 1024);
     };
     auto dma_v = [&](int raw, int t, unsigned char* to) __attribute__((always_inline)) {
-      const char* const src = source(a.v_pool, raw, t);
-#pragma unroll
-      for (int i = 0; i < kOps; ++i) dma_1k(src + i * 1024 + v_src, to + (wave * kOps + i) * 1024);
+      const __amdgpu_buffer_rsrc_t src = source(a.v_pool, raw, t);
+      unsigned char* const at = to + wave * kOps * 1024;
+      dma_1k<0>(src, v_src, at);
+      if constexpr (kOps > 1) dma_1k<1024>(src, v_src, at);
+      if constexpr (kOps > 2) dma_1k<2048>(src, v_src, at);
+      if constexpr (kOps > 3) dma_1k<3072>(src, v_src, at);
     };
     auto raw_id = [&](int t) __attribute__((always_inline)) { return row.raw(min(t, t1 - 1) * S::kKeys + 16 * sub16); };
 
@@ -174,49 +179,61 @@ __global__ __launch_bounds__(kAttendThreads, 1) void k_attend_rows(AttendArgs a,
       return value_operand<CT>(
           *reinterpret_cast<const typename TT::V*>(vb + ((sub * 4 + 2 * sl + h) * D + 32 * db + col) * (8 * kEs)));
     };
-    // One tile, in (kb, vb); the other buffers receive the next.
-    auto step = [&](int t, int id_next, unsigned char* kb, unsigned char* vb, unsigned char* kn, unsigned char* vn) __attribute__((always_inline)) {
-      wait_vmem();         // this wave's part of the tile has landed
-      barrier_lds_only();  // everybody's has, and nobody reads the other buffers any more
-      if (t + 1 < t1) {
-        dma_k(id_next, t + 1, kn);
-        dma_v(id_next, t + 1, vn);
-      }
+    // Waits until at most the youngest two of this wave's DMA groups (of keys or of values)
+    // are on their way.  Past the last tile the last one is brought again, so that there
+    // are always as many and the compiler, which counts too, adds no waits of its own.
+    auto landed = [&]() __attribute__((always_inline)) { wait_vmem_n<2 * kOps>(); };
+    // One tile, keys in kb and values in vb; v_next receives the next tile's values and kb,
+    // once read, the keys of the one after.  Every group of DMA is sent one and a half
+    // tiles before it is used.
+    auto step = [&](int t, int id1, int id2, unsigned char* kb, unsigned char* vb, unsigned char* v_next) __attribute__((always_inline)) {
+      landed();            // this wave's part of the keys
+      barrier_lds_only();  // everybody's, and the last tile's values are read
+      dma_v(id1, t + 1, v_next);
       const int key0 = t * S::kKeys;
+      const bool on = key0 < some_hi && key0 + S::kKeys > some_lo;  // something that this wave's rows see
+      f32x16_t w[S::kSubs];
+      if (on) {
+#pragma unroll
+        for (int sub = 0; sub < S::kSubs; ++sub) scores(kb, sub, w[sub]);
+        // LDS reads run kAhead fragments before their products
+        constexpr int kReads = S::kSubs * TT::kK, kMma = CT == DSPARK_BF16 ? 1 : 2;
+        schedule<kLdsRead, kAhead>();
+#pragma unroll
+        for (int i = 0; i < kReads - kAhead; ++i) {
+          schedule<kMfma, kMma>();
+          schedule<kLdsRead, 1>();
+        }
+        schedule<kMfma, kAhead * kMma>();
+        if (key0 < all_lo || key0 + S::kKeys > all_hi) {
+#pragma unroll
+          for (int sub = 0; sub < S::kSubs; ++sub)
+            mask_scores<false>(w[sub], row_lo - (key0 + 32 * sub), row_hi - (key0 + 32 * sub), h);
+        }
+        const float fade = raise_max(w, run, ks);
+        if (__any(fade != 1.f)) {
+#pragma unroll
+          for (int db = 0; db < TT::kBlocks; ++db) acc[db] *= fade;
+        }
+      }
+      landed();            // this wave's part of the values
+      barrier_lds_only();  // everybody's, and the keys are read
+      dma_k(id2, t + 2, kb);
       if (key0 < g.all_lo || key0 + S::kKeys > g.all_hi) {
         // a tile that not all rows see whole: its values are made finite, in place
-        uint4* const mine = reinterpret_cast<uint4*>(vb);
+        uint4* const mine = reinterpret_cast<uint4*>(vb) + threadIdx.x;
         uint32_t bits = 0;
-        for (int i = threadIdx.x; i < S::kBytes / 16; i += kAttendThreads) find_nonfinite<CT>(mine[i], bits);
+#pragma unroll
+        for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i) find_nonfinite<CT>(mine[i * kAttendThreads], bits);
         if (__any(bits & kOdd<CT>)) {
           odd = 1;
-          for (int i = threadIdx.x; i < S::kBytes / 16; i += kAttendThreads) mine[i] = finite_part<CT>(mine[i]);
+#pragma unroll 1
+          for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i)
+            mine[i * kAttendThreads] = finite_part<CT>(mine[i * kAttendThreads]);
         }
         barrier_lds_only();
       }
-      if (key0 >= some_hi || key0 + S::kKeys <= some_lo) return;  // nothing that this wave's rows see
-      f32x16_t w[S::kSubs];
-#pragma unroll
-      for (int sub = 0; sub < S::kSubs; ++sub) scores(kb, sub, w[sub]);
-      // LDS reads run kAhead fragments before their products
-      constexpr int kReads = S::kSubs * TT::kK, kMma = CT == DSPARK_BF16 ? 1 : 2;
-      schedule<kLdsRead, kAhead>();
-#pragma unroll
-      for (int i = 0; i < kReads - kAhead; ++i) {
-        schedule<kMfma, kMma>();
-        schedule<kLdsRead, 1>();
-      }
-      schedule<kMfma, kAhead * kMma>();
-      if (key0 < all_lo || key0 + S::kKeys > all_hi) {
-#pragma unroll
-        for (int sub = 0; sub < S::kSubs; ++sub)
-          mask_scores<false>(w[sub], row_lo - (key0 + 32 * sub), row_hi - (key0 + 32 * sub), h);
-      }
-      const float fade = raise_max(w, run, ks);
-      if (__any(fade != 1.f)) {
-#pragma unroll
-        for (int db = 0; db < TT::kBlocks; ++db) acc[db] *= fade;
-      }
+      if (!on) return;
       // the weights of the first half, then its product with the values next to the
       // weights of the second half
 #pragma unroll
@@ -242,19 +259,22 @@ __global__ __launch_bounds__(kAttendThreads, 1) void k_attend_rows(AttendArgs a,
         }
     };
 
-    // ---- tiles; page ids come over the scalar cache two tiles ahead
-    int id = raw_id(t0), id1 = raw_id(t0 + 1);
+    // ---- tiles; page ids come over the scalar cache ahead of their use
+    int id0 = raw_id(t0), id1 = raw_id(t0 + 1), id2 = raw_id(t0 + 2);
     barrier_lds_only();  // the last segment's tiles are read
     if (threadIdx.x == 0) odd = 0;
-    dma_k(id, t0, k0);
-    dma_v(id, t0, v0);
+    dma_k(id0, t0, k0);
+    dma_v(id0, t0, v0);
+    dma_k(id1, t0 + 1, k1);
     for (int t = t0; t < t1; t += 2) {
-      id = raw_id(t + 2);
-      step(t, id1, k0, v0, k1, v1);
+      const int id3 = raw_id(t + 3), id4 = raw_id(t + 4);
+      step(t, id1, id2, k0, v0, v1);
       if (t + 1 == t1) break;
-      id1 = raw_id(t + 3);
-      step(t + 1, id, k1, v1, k0, v0);
+      step(t + 1, id2, id3, k1, v1, v0);
+      id1 = id3;
+      id2 = id4;
     }
+    wait_vmem();  // what was brought again
 
     // ---- results
     const bool whole = take == g.tiles;
