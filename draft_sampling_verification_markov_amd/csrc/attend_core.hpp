@@ -577,10 +577,10 @@ __device__ __forceinline__ void put_record(const Partials& ws, const Start& s, i
 
 // Joins the partial results of the segment that worker blockIdx.x's first unit lies
 // in, if the worker is the segment's second one.  A row's parts (m, l, O) add up as
-// sum exp2(m - M) (l, O), M the largest m, in a fixed order.  Few parts: a group of
-// D / 4 threads takes a row, 8 rows a workgroup.  Many (a long context dealt to many
-// workers): the workgroup takes a row, its groups the parts in turn.
-constexpr int kJoinY = 8;
+// sum exp2(m - M) (l, O), M the largest m, in a fixed order.  Groups of D / 4 threads
+// take a row each; where there are many parts and few rows (tokens over a long context
+// dealt to many workers) the workgroup takes a row, its groups the parts in turn.
+constexpr int join_groups(int rows) { return rows > 64 ? 16 : 8; }  // workgroups of a segment
 constexpr int kFewParts = 8, kMaxParts = 4 * kCUs;  // (the most workers)
 template <int CT, int D, int ROWS>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Split p) {
@@ -610,11 +610,13 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
     store4<CT>(a.out, row * a.out_stride + (size_t)hq * D + 4 * lane, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
     if (a.lse && lane == 0) a.lse[row * a.c.Hq + hq] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2f;
   };
-  if (parts <= kFewParts) {
-    for (int rho = blockIdx.y * kGroups + group; rho < g.rows; rho += kJoinY * kGroups) {
+  if (parts <= kFewParts || g.rows > (int)gridDim.y) {
+    for (int rho = blockIdx.y * kGroups + group; rho < g.rows; rho += gridDim.y * kGroups) {
       float top = -INFINITY, l = 0.f;
+#pragma unroll 8
       for (int i = 0; i < parts; ++i) top = fmaxf(top, slot(i)[(size_t)ROWS * D + 2 * rho]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
       for (int i = 0; i < parts; ++i) {
         const float* s = slot(i);
         const float2 ml = *reinterpret_cast<const float2*>(s + (size_t)ROWS * D + 2 * rho);
@@ -628,7 +630,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
   }
   __shared__ float factor[kMaxParts], sh[kAttendThreads / 64];
   __shared__ float4 so[kGroups][kLanes];
-  for (int rho = blockIdx.y; rho < g.rows; rho += kJoinY) {
+  for (int rho = blockIdx.y; rho < g.rows; rho += gridDim.y) {
     float2 ml[kMaxParts / kAttendThreads];
 #pragma unroll
     for (int e = 0; e < kMaxParts / kAttendThreads; ++e) {

@@ -41,7 +41,7 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   k_attend_keys<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, NB * 16><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, NB * 16><<<dim3(pl.split.workers, join_groups(NB * 16)), kAttendThreads, 0, s>>>(a, pl.split);
   return hipGetLastError();
 }
 
@@ -54,7 +54,7 @@ hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   k_attend_rows<CT, D><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, S::kRows><<<dim3(pl.split.workers, kJoinY), kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, S::kRows><<<dim3(pl.split.workers, join_groups(S::kRows)), kAttendThreads, 0, s>>>(a, pl.split);
   return hipGetLastError();
 }
 
