@@ -49,12 +49,12 @@ struct KeysTile {
   __device__ __forceinline__ static constexpr int key_of_reg(int t, int i) { return kF32 ? 16 * t + i : 4 * t + i; }
 };
 
-// A load of what no other wave reads soon (the streaming policy: 256 one-token requests
-// 421 -> 402 us, 200,000 e4m3 keys 75 -> 68 us).
-template <typename V>
-__device__ __forceinline__ V load_once(const char* p) {
+// A load of keys or values; ONCE: with the streaming policy.
+template <typename V, bool ONCE>
+__device__ __forceinline__ V load_key(const char* p) {
   typedef unsigned words_t __attribute__((ext_vector_type(sizeof(V) / 4)));
-  return __builtin_bit_cast(V, __builtin_nontemporal_load(reinterpret_cast<const words_t*>(p)));
+  const words_t* q = reinterpret_cast<const words_t*>(p);
+  return __builtin_bit_cast(V, ONCE ? __builtin_nontemporal_load(q) : *q);
 }
 
 // The largest, or the sum, of the four lanes that hold a row.
@@ -67,7 +67,7 @@ __device__ __forceinline__ float groups_sum(float x) {
   return halves32_sum(a.x + a.y);
 }
 
-template <int CT, int D, int NB, int OCC>
+template <int CT, int D, int NB, int OCC, bool ONCE>
 __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs a, Split p) {
   using TT = KeysTile<CT, D>;
   constexpr bool kF32 = TT::kF32;
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
         const int key = TT::key_of_row(t, col);
         const char* src = kp + (kF32 ? half[t] : (col < 8 ? half[0] : half[1])) + (key & 15) * (D * kEs) + 16 * g16;
 #pragma unroll
-        for (int x = 0; x < TT::kK; ++x) k[t][x] = load_once<uint4>(src + 64 * x);
+        for (int x = 0; x < TT::kK; ++x) k[t][x] = load_key<uint4, ONCE>(src + 64 * x);
       }
     };
     uint4 k[2][TT::kK];
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
                                  : vp + (g16 < 2 ? half[0] : half[1]) + ((g16 & 1) * D + col) * (8 * kEs);
 #pragma unroll
           for (int db = 0; db < TT::kBlocks; ++db)
-            v[t][db] = load_once<typename TT::V>(src + db * (16 * 8 * kEs));
+            v[t][db] = load_key<typename TT::V, ONCE>(src + db * (16 * 8 * kEs));
         }
       }
       f32x4_t w[NB][2];

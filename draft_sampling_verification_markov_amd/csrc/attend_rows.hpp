@@ -29,7 +29,7 @@ struct RowsShape {
   static constexpr int kBytes = kKeys * D * kEs;             // of the keys (or the values) of a tile
   static constexpr int kPieces = D * kEs / 16;               // of a key
   static constexpr int kOps = kBytes / 1024 / 4;               // DMA instructions a wave, keys (or values)
-  static constexpr int kPerCu = D == 256 ? 1 : 2;            // workgroups that a CU holds
+  static constexpr int kPerCu = 2;                           // workgroups that a CU holds
   // 64 banks of 4 bytes: 16 pieces a cycle, one or more rows of keys
   __device__ __forceinline__ static int swizzle(int r) { return kPieces >= 16 ? r & 15 : (r / (16 / kPieces)) & (kPieces - 1); }
 };
@@ -44,13 +44,15 @@ __device__ __forceinline__ void schedule() {
 
 // 64 lanes x 16 bytes at the lanes' offsets + AT of the buffer to the 1 KB of LDS at AT, in
 // lane order (the instruction's offset counts on both sides)
-template <int AT>
+template <int AT, bool ONCE>
 __device__ __forceinline__ void dma_1k(__amdgpu_buffer_rsrc_t src, int offset, unsigned char* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, offset, 0, AT, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, offset, 0, AT,
+                                           ONCE ? 2 : 0);
 }
 
-template <int CT, int D>
-__global__ __launch_bounds__(kAttendThreads, 1) void k_attend_rows(AttendArgs a, Split p) {
+// ONCE: keys and values with the streaming policy
+template <int CT, int D, bool ONCE>
+__global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_rows(AttendArgs a, Split p) {
   using S = RowsShape<CT, D>;
   using TT = Tile<CT, D>;
   constexpr int kQ = q_regs<CT, D>(), kRows = S::kRows, kEs = S::kEs;
@@ -94,8 +96,8 @@ __global__ __launch_bounds__(kAttendThreads, 1) void k_attend_rows(AttendArgs a,
     k_src[i] = (key_of_row<false>(r & 31) & 15) * (D * kEs) + piece * 16;
   }
   v_src = ((wave * kOps * 64 + lane) % (S::kPieces * 16)) * 16;
-  // reading: this lane's K row is col of each half tile, pieces 2 x + h
-  const int k_row = col * (S::kPieces * 16), k_swz = S::swizzle(col);
+  // reading: this lane's K row is col of each half tile, pieces 2 x + h, at k_at ^ 32 x
+  const int k_at = col * (S::kPieces * 16) + ((h ^ S::swizzle(col)) << 4);
 
   while (true) {
     const int t0 = g.tile0 + s.skip, take = min(left, g.tiles - s.skip), t1 = t0 + take;
@@ -150,23 +152,25 @@ __global__ __launch_bounds__(kAttendThreads, 1) void k_attend_rows(AttendArgs a,
     auto dma_k = [&](int raw, int t, unsigned char* to) __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t src = source(a.k_pool, raw, t);
 #pragma unroll
-      for (int i = 0; i < kOps; ++i) dma_1k<0>(src, k_src[i], to + (wave * kOps + i) * 1024);
+      for (int i = 0; i < kOps; ++i) dma_1k<0, ONCE>(src, k_src[i], to + (wave * kOps + i) * 1024);
     };
     auto dma_v = [&](int raw, int t, unsigned char* to) __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t src = source(a.v_pool, raw, t);
       unsigned char* const at = to + wave * kOps * 1024;
-      dma_1k<0>(src, v_src, at);
-      if constexpr (kOps > 1) dma_1k<1024>(src, v_src, at);
-      if constexpr (kOps > 2) dma_1k<2048>(src, v_src, at);
-      if constexpr (kOps > 3) dma_1k<3072>(src, v_src, at);
+      dma_1k<0, ONCE>(src, v_src, at);
+      if constexpr (kOps > 1) dma_1k<1024, ONCE>(src, v_src, at);
+      if constexpr (kOps > 2) dma_1k<2048, ONCE>(src, v_src, at);
+      if constexpr (kOps > 3) dma_1k<3072, ONCE>(src, v_src, at);
     };
     auto raw_id = [&](int t) __attribute__((always_inline)) { return row.raw(min(t, t1 - 1) * S::kKeys + 16 * sub16); };
 
     auto scores = [&](const unsigned char* kb, int sub, f32x16_t& w) __attribute__((always_inline)) {
       w = f32x16_t{};
+      int at = k_at;
+      if (D == 256) asm volatile("" : "+v"(at));  // no room for 16 addresses kept from tile to tile
 #pragma unroll
       for (int x = 0; x < TT::kK; ++x) {
-        const uint4 k = *reinterpret_cast<const uint4*>(kb + sub * 32 * (D * kEs) + k_row + (((2 * x + h) ^ k_swz) << 4));
+        const uint4 k = *reinterpret_cast<const uint4*>(kb + sub * 32 * (D * kEs) + (at ^ (32 * x)));
         if constexpr (CT == DSPARK_BF16) {
           w = mma(as_bf16x8(k), as_bf16x8(q[x]), w);
         } else {

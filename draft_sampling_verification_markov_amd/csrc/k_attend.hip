@@ -33,29 +33,37 @@ Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int 
   return pl;
 }
 
+// Keys that one workgroup reads, and that the 256 MB last-level cache does not hold until
+// the next call, are read with the streaming policy: 256 requests x 17 rows 205 -> 192 us,
+// 256 x 1 421 -> 402.  For others it costs: prompts, whose row tiles meet in L2, 567 -> 603,
+// 72 MB of keys 28 -> 33.
+bool read_once(const dspark_cache& C, const Plan& pl) {
+  return pl.split.row_tiles == 1 && 2 * page_bytes(C) * C.n_pages > ((size_t)256 << 20);
+}
+
+template <int CT, int D, int ROWS, typename Kernel>
+hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, const Plan& pl, Kernel kernel, hipStream_t s) {
+  if (!pl.split.workers) {
+    kernel<<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
+    return hipGetLastError();
+  }
+  kernel<<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
+  k_attend_join<CT, D, ROWS><<<dim3(pl.split.workers, join_groups(ROWS)), kAttendThreads, 0, s>>>(a, pl.split);
+  return hipGetLastError();
+}
+
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys);
-  if (!pl.split.workers) {
-    k_attend_keys<CT, D, NB, OCC><<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
-    return hipGetLastError();
-  }
-  k_attend_keys<CT, D, NB, OCC><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, NB * 16><<<dim3(pl.split.workers, join_groups(NB * 16)), kAttendThreads, 0, s>>>(a, pl.split);
-  return hipGetLastError();
+  return run_plan<CT, D, NB * 16>(
+      C, a, pl, read_once(C, pl) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
 
 template <int CT, int D>
 hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   using S = RowsShape<CT, D>;
   const Plan pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows);
-  if (!pl.split.workers) {
-    k_attend_rows<CT, D><<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
-    return hipGetLastError();
-  }
-  k_attend_rows<CT, D><<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, S::kRows><<<dim3(pl.split.workers, join_groups(S::kRows)), kAttendThreads, 0, s>>>(a, pl.split);
-  return hipGetLastError();
+  return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 
 // Workgroups of k_attend_keys that a CU holds, by their registers.
