@@ -30,13 +30,13 @@ struct RowsShape {
   static constexpr int kPieces = D * kEs / 16;               // of a key
   static constexpr int kOps = kBytes / 1024 / 4;               // DMA instructions a wave, keys (or values)
   static constexpr int kPerCu = 2;                           // workgroups that a CU holds
+  static constexpr int kAhead = D == 256 ? 3 : 4;            // LDS reads before their products (more spill at 256)
   // 64 banks of 4 bytes: 16 pieces a cycle, one or more rows of keys
   __device__ __forceinline__ static int swizzle(int r) { return kPieces >= 16 ? r & 15 : (r / (16 / kPieces)) & (kPieces - 1); }
 };
 
 // Order of instructions that the scheduler is asked for: the next `n` of a kind.
 constexpr int kValu = 0x2, kMfma = 0x8, kLdsRead = 0x100;
-constexpr int kAhead = 4;
 template <int KIND, int N>
 __device__ __forceinline__ void schedule() {
   __builtin_amdgcn_sched_group_barrier(KIND, N, 0);
@@ -202,13 +202,13 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
         for (int sub = 0; sub < S::kSubs; ++sub) scores(kb, sub, w[sub]);
         // LDS reads run kAhead fragments before their products
         constexpr int kReads = S::kSubs * TT::kK, kMma = CT == DSPARK_BF16 ? 1 : 2;
-        schedule<kLdsRead, kAhead>();
+        schedule<kLdsRead, S::kAhead>();
 #pragma unroll
-        for (int i = 0; i < kReads - kAhead; ++i) {
+        for (int i = 0; i < kReads - S::kAhead; ++i) {
           schedule<kMfma, kMma>();
           schedule<kLdsRead, 1>();
         }
-        schedule<kMfma, kAhead * kMma>();
+        schedule<kMfma, S::kAhead * kMma>();
         if (key0 < all_lo || key0 + S::kKeys > all_hi) {
 #pragma unroll
           for (int sub = 0; sub < S::kSubs; ++sub)
@@ -251,14 +251,14 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
         }
       }
       constexpr int kValues = 2 * TT::kBlocks, kSoft = 58;
-      schedule<kLdsRead, kAhead>();
+      schedule<kLdsRead, S::kAhead>();
       schedule<kValu, kSoft>();
 #pragma unroll
       for (int sub = 0; sub < S::kSubs; ++sub)
 #pragma unroll
         for (int i = 0; i < kValues; ++i) {
           schedule<kMfma, 1>();
-          if (sub * kValues + i + kAhead < S::kSubs * kValues) schedule<kLdsRead, 1>();
+          if (sub * kValues + i + S::kAhead < S::kSubs * kValues) schedule<kLdsRead, 1>();
           if (sub + 1 < S::kSubs) schedule<kValu, kSoft / kValues>();
         }
     };

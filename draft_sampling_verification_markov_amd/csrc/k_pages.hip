@@ -24,12 +24,13 @@ __device__ __forceinline__ uint32_t f8_pair(float x, float y) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, y, 0, false) & 0xFFFFu;
 }
 
-// One thread carries 2 coordinates of the 8 tokens of a value group (the v_pool's
-// unit [D][8]): it reads 8 rows, neighbouring threads neighbouring coordinates, and
-// writes 2 x 8 tokens, so a full group leaves as whole 16-byte pieces and a single
-// token as 2-element stores inside one 8 * D element region.  The keys of the
-// same 8 tokens are copied row by row.  Bound by the bytes of the new rows (read
-// once, written once); for a few tokens by the latency of table -> page -> store.
+// A workgroup writes 8-token groups (the v_pool's unit [D][8]) of a few heads, D / 2
+// threads each.  Values: a thread carries 2 coordinates, reads 8 rows (neighbouring
+// threads neighbouring coordinates) and writes 2 x 8 tokens as whole 16-byte pieces; of
+// a group that is new in part it reads the old pieces too and merges, since 2-byte
+// stores cost more (256 x 17 rows 13.6 us with them).  Keys: rows copied in 16-byte
+// pieces.  All loads are issued before the first use.  Bound by the bytes of the new
+// rows; for a few tokens by the latency of length -> table -> rows -> store.
 template <int CT>
 struct CacheType;
 template <>
@@ -67,6 +68,7 @@ template <int CT, int D>
 __device__ __forceinline__ void append_group(const AppendArgs& a, int b, int gi) {
   using T = typename CacheType<CT>::T;
   constexpr int kPerHead = D / 2;  // threads of one head
+  constexpr int kData = CT == DSPARK_F32 ? 4 : 2;
   const CacheView& c = a.c;
   const int n = c.rows(b), len = c.len(b);
   const int pos0 = len - n;                       // of token 0; may be negative
@@ -81,59 +83,71 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int b, int gi)
   if ((unsigned)page >= (unsigned)c.n_pages) return;
   const int off = j0 & ((1 << c.page_shift) - 1);
   const size_t block = ((size_t)page * c.Hkv + head) << c.page_shift;  // tokens
-  T* const kd = static_cast<T*>(a.k_pool) + (block + off) * D + d;
+  T* const kd = static_cast<T*>(a.k_pool) + (block + off) * D;
   T* const vd = static_cast<T*>(a.v_pool) + (block + off) * D + (size_t)d * 8;
   const float ks = CT == DSPARK_F8E4M3 ? a.k_scale[head] : 1.f, vs = CT == DSPARK_F8E4M3 ? a.v_scale[head] : 1.f;
   const long long row0 = c.first_row(b) + (j0 - pos0);
-  // all loads at once: rows that are not there are read as the nearest one that is
-  typename DataPair<CT>::T kw[8], vw[8];
-  bool has[8], all = true;
+  // tokens of the group that are new and have a row; the others read the nearest row that is there
+  auto has = [&](int t) { return j0 + t >= lo && j0 + t < hi && c.has_row(row0 + t); };
+  auto row_of = [&](int t) {
+    const long long near = row0 + min(max(t, lo - j0), hi - 1 - j0);
+    return near < 0 ? 0 : near < c.n_rows ? near : (long long)c.n_rows - 1;
+  };
+  constexpr int kEs = sizeof(T), kPieces = D * kEs / 16;  // 16-byte pieces of a key
+  constexpr int kWords = CT == DSPARK_F8E4M3 ? 2 : 1;     // 16-byte words of data for one
+  uint4 kw[kEs][kWords];
+#pragma unroll
+  for (int i = 0; i < kEs; ++i) {
+    const int at = i * kPerHead + threadIdx.x % kPerHead;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) +
+                                                      (row_of(at / kPieces) * a.k_stride + head * D) * kData) +
+                       at % kPieces * kWords;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) kw[i][w] = src[w];
+  }
+  typename DataPair<CT>::T vw[8];
+  bool all = true;
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    const long long r = row0 + t, near = row0 + min(max(t, lo - j0), hi - 1 - j0);
-    has[t] = j0 + t >= lo && j0 + t < hi && c.has_row(r);
-    all = all && has[t];
-    const long long safe = near < 0 ? 0 : near < c.n_rows ? near : c.n_rows - 1;
-    kw[t] = DataPair<CT>::load(a.k, safe * a.k_stride + head * D + d);
-    vw[t] = DataPair<CT>::load(a.v, safe * a.v_stride + head * D + d);
+    all = all && has(t);
+    vw[t] = DataPair<CT>::load(a.v, row_of(t) * a.v_stride + head * D + d);
   }
-  T kx[8][2], vx[8][2];
+  constexpr int kLine = 16 * kEs / 16;  // 16-byte words of 2 coordinates x 8 tokens
+  uint4 old[kLine];
+#pragma unroll
+  for (int i = 0; i < kLine; ++i) old[i] = reinterpret_cast<const uint4*>(vd)[i];
+
+#pragma unroll
+  for (int i = 0; i < kEs; ++i) {
+    const int at = i * kPerHead + threadIdx.x % kPerHead, t = at / kPieces;
+    uint4 x = kw[i][0];
+    if constexpr (CT == DSPARK_F8E4M3) {
+      const uint32_t in[8] = {kw[i][0].x, kw[i][0].y, kw[i][0].z, kw[i][0].w,
+                              kw[i][1].x, kw[i][1].y, kw[i][1].z, kw[i][1].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = f8_pair(bf16_lo(in[2 * j]) / ks, bf16_hi(in[2 * j]) / ks) |
+               f8_pair(bf16_lo(in[2 * j + 1]) / ks, bf16_hi(in[2 * j + 1]) / ks) << 16;
+      x = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (has(t)) reinterpret_cast<uint4*>(kd)[at] = x;
+  }
+  T line[16];
+  __builtin_memcpy(line, old, sizeof(line));
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    store_type<CT>(kw[t], ks, kx[t]);
-    store_type<CT>(vw[t], vs, vx[t]);
+    T x[2];
+    store_type<CT>(vw[t], vs, x);
+    const bool is = all || has(t);
+    line[t] = is ? x[0] : line[t];
+    line[8 + t] = is ? x[1] : line[8 + t];
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
-    if (has[t]) {
-      if constexpr (CT == DSPARK_F32)
-        *reinterpret_cast<uint2*>(kd + t * D) = make_uint2(kx[t][0], kx[t][1]);
-      else if constexpr (CT == DSPARK_BF16)
-        *reinterpret_cast<uint32_t*>(kd + t * D) = kx[t][0] | (uint32_t)kx[t][1] << 16;
-      else
-        *reinterpret_cast<uint16_t*>(kd + t * D) = (uint16_t)(kx[t][0] | kx[t][1] << 8);
-    }
-  if (all) {
-    T line[16];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      line[t] = vx[t][0];
-      line[8 + t] = vx[t][1];
-    }
-    constexpr int kPieces = (int)sizeof(line) / 16;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      uint4 w;
-      __builtin_memcpy(&w, reinterpret_cast<const char*>(line) + 16 * i, 16);
-      reinterpret_cast<uint4*>(vd)[i] = w;
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (has[t]) {
-        vd[t] = vx[t][0];
-        vd[8 + t] = vx[t][1];
-      }
+  for (int i = 0; i < kLine; ++i) {
+    uint4 w;
+    __builtin_memcpy(&w, reinterpret_cast<const char*>(line) + 16 * i, 16);
+    reinterpret_cast<uint4*>(vd)[i] = w;
   }
 }
 
