@@ -4,6 +4,10 @@ Plumbing around the binding: uploads host arrays (bf16 given as raw uint16
 bit patterns, fp32 as float32), allocates the caller-owned outputs and the
 workspace with torch, and issues dspark_draft -> dspark_schedule ->
 dspark_verify on the current stream.
+
+PagedCache owns the buffers of the paged key/value cache, and run_cached_cycle
+is the cycle with the target's forward pass over that cache between the schedule
+and the verification.
 """
 from __future__ import annotations
 
@@ -97,3 +101,74 @@ def run_cycle(P, x: CycleInputs, o: CycleOutputs, stream=None, path: int = dspar
     draft(P, x, o, stream, path)
     schedule(P, x, o, stream)
     verify(P, x, o, stream)
+
+
+class PagedCache:
+    """Pools, page tables, lengths and references of a paged cache, and its calls.
+
+    table, length and ref are the present sequences; update writes the other set of
+    them and swaps the two (so a captured graph holds an even number of updates)."""
+
+    def __init__(self, C: dspark.Cache, max_new: int, device="cuda", k_scale=None, v_scale=None):
+        self.C, self.max_new = C, int(max_new)
+        i32 = torch.int32
+        self.k = torch.zeros(C.k_shape, dtype=torch.uint8, device=device).to(C.cache_type) if C.cache_dtype == dspark.F8E4M3 \
+            else torch.zeros(C.k_shape, dtype=C.cache_type, device=device)
+        self.v = torch.zeros_like(self.k).view(C.v_shape)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        if C.cache_dtype == dspark.F8E4M3:
+            one = torch.ones(C.Hkv, dtype=torch.float32, device=device)
+            self.k_scale = one if k_scale is None else k_scale
+            self.v_scale = one if v_scale is None else v_scale
+        self._sets = [(torch.full((C.B, C.max_pages), -1, dtype=i32, device=device),
+                       torch.zeros(C.B, dtype=i32, device=device), torch.zeros(C.n_pages, dtype=i32, device=device))
+                      for _ in range(2)]
+        self.n_short = torch.zeros(1, dtype=i32, device=device)
+        self.n_live = torch.zeros(1, dtype=i32, device=device)
+        nbytes = dspark.cache_workspace_bytes(C, self.max_new)
+        if nbytes == 0:
+            raise ValueError("invalid cache")
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+    table = property(lambda self: self._sets[0][0])
+    length = property(lambda self: self._sets[0][1])
+    ref = property(lambda self: self._sets[0][2])
+
+    def update(self, new_len, parent=None, stream=None):
+        """Every slot's next sequence (dspark_cache_update); n_short tells the pages that were missing."""
+        now, new = self._sets
+        dspark.cache_update(self.C, parent, new_len, *now, *new, self.n_short, self.k, self.v, self.workspace, stream)
+        self._sets.reverse()
+
+    def compact(self, stream=None):
+        """Live pages to the lowest ids (dspark_cache_compact); n_live tells how many there are."""
+        now, new = self._sets
+        dspark.cache_compact(self.C, *now, new[0], new[2], self.n_live, self.k, self.v, self.workspace, stream)
+        self._sets = [(new[0], now[1], new[2]), (now[0], new[1], now[2])]
+
+    def append(self, layer: int, k, v, n_new=None, row_start=None, stream=None):
+        dspark.cache_append(self.C, layer, k, v, n_new, row_start, self.max_new, self.length, self.table,
+                            self.k_scale, self.v_scale, self.k, self.v, stream)
+
+    def attend(self, layer: int, q, out, lse=None, n_new=None, row_start=None, scale=None, causal=True, window=0,
+               stream=None):
+        dspark.cache_attend(self.C, layer, q, n_new, row_start, self.max_new, self.length, self.table, self.k, self.v,
+                            self.k_scale, self.v_scale, out, lse, self.workspace, scale, causal, window, stream)
+
+
+def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forward, path: int = dspark.DRAFT_AUTO):
+    """One cycle over a paged cache, on the current stream, without reading anything back.
+
+    After the schedule the cache grows by the n_sched + 1 rows of every request (the anchor and its
+    drafts); forward(tokens [B][K + 1], n_new [B]) runs the target over them (cache.append and
+    cache.attend per layer, rows b * (K + 1) ..) and leaves its logits in x.Zt; after the verification
+    the cache keeps the anchor and the accepted drafts.  Where the pool cannot hold a request's rows,
+    cache.n_short is positive, n_new[b] is 0 and what the cycle emits for that request is unspecified."""
+    draft(P, x, o, path=path)
+    schedule(P, x, o)
+    before = cache.length
+    cache.update(before + o.n_sched + 1)
+    n_new = cache.length - before
+    forward(torch.cat([x.anchor[:, None], o.tok], 1), n_new)
+    verify(P, x, o)
+    cache.update(torch.minimum(before + o.n_acc + 1, cache.length))

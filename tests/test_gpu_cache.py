@@ -267,6 +267,24 @@ def test_append_f8_rounds_every_value_as_defined(ds):
     np.testing.assert_array_equal(vp.cpu()[0, :, 0, 0, :, 2].double().numpy(), want)
 
 
+@pytest.mark.parametrize("scale", [0.02, 1.0 / 3.0, 0.03999999, 7.7e-3, 1e3, 3e-20, 2e-39])
+def test_append_f8_quotients(ds, scale):
+    # all bf16 values over several scales: the e4m3 value of the rounded fp32 quotient, bit for bit
+    D, B = 256, 256
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(B, 1, D)
+    C = ds.Cache.make(B, B, 16, 1, 1, 1, 1, D, cache="f8")
+    kp = torch.zeros(C.k_shape, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vp = torch.zeros(C.v_shape, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.full((1,), scale, device="cuda")
+    ds.cache_append(C, 0, x.cuda(), x.cuda(), None, None, 1, cu.i32(np.full(B, 6)), cu.i32(np.arange(B)[:, None]), s, s,
+                    kp, vp)
+    with np.errstate(over="ignore", invalid="ignore"):
+        q = x.float().numpy()[:, 0] / np.float32(scale)
+    want = oc.round_f8(q.astype(np.float64))
+    np.testing.assert_array_equal(kp.cpu()[0, :, 0, 5].double().numpy(), want)
+    np.testing.assert_array_equal(vp.cpu()[0, :, 0, 0, :, 5].double().numpy(), want)
+
+
 def test_append_leaves_out_bad_ids(ds):
     c = cu.make(41, "bf16", 16, 64, 1, 1, [3, 3], [20, 20], poison=False)
     c.table[1] = [c.k_pool.shape[1], -1]
