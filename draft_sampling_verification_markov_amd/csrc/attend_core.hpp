@@ -101,7 +101,7 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p
 struct Start {
   int b, head, row_tile;
   int skip;   // units of the segment before the worker's first
-  int count;  // the worker's units
+  long long count;  // the worker's units
   int workers;  // that have any
   long long unit, total;
 };
@@ -154,7 +154,7 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   s.workers = (int)(s.total < p.workers ? s.total : p.workers);
   if (worker >= s.workers) return s;
   s.unit = worker * s.total / s.workers;
-  s.count = (int)((worker + 1) * s.total / s.workers - s.unit);
+  s.count = (worker + 1) * s.total / s.workers - s.unit;
   long long before = 0;
   for (long long c = 0; c < pairs; c += THREADS) {
     const long long i = c + threadIdx.x;
@@ -217,7 +217,7 @@ __device__ __forceinline__ Start whole_segment(const AttendArgs& a, const Split&
   s.row_tile = p.row_tiles - 1 - (int)(slot % p.row_tiles);
   s.head = (int)(pair % a.c.Hkv);
   s.b = (int)(pair / a.c.Hkv);
-  s.count = 0x7fffffff;
+  s.count = 0x7fffffffffffffffLL;
   return s;
 }
 // workgroups of such a launch: the pairs rounded up to whole rounds of the XCDs

@@ -95,14 +95,14 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     s = whole_segment(a, p);
     if (s.b >= c.B) return;
   }
-  int left = s.count;
+  long long left = s.count;
   bool first_segment = true;
   Geometry g = geometry<kRows>(a, p, s.b, s.row_tile);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
   if (g.tiles == 0) return;  // a direct workgroup without rows
 
   while (true) {
-    const int t0 = g.tile0 + s.skip, take = min(left, g.tiles - s.skip), t1 = t0 + take;
+    const int t0 = g.tile0 + s.skip, take = (int)min(left, (long long)(g.tiles - s.skip)), t1 = t0 + take;
     const int head = s.head, blocks = (g.rows + 15) >> 4;
 
     // ---- keys: this wave's tiles, every fourth one of the units that some row sees.

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     s = whole_segment(a, p);
     if (s.b >= c.B) return;
   }
-  int left = s.count;
+  long long left = s.count;
   bool first_segment = true;
   Geometry g = geometry<kRows>(a, p, s.b, s.row_tile);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
   const int k_at = col * (S::kPieces * 16) + ((h ^ S::swizzle(col)) << 4);
 
   while (true) {
-    const int t0 = g.tile0 + s.skip, take = min(left, g.tiles - s.skip), t1 = t0 + take;
+    const int t0 = g.tile0 + s.skip, take = (int)min(left, (long long)(g.tiles - s.skip)), t1 = t0 + take;
     const int head = s.head;
     const Masks mask{a.causal, a.window, c.len(g.b)};
     const int G = c.Hq / c.Hkv;

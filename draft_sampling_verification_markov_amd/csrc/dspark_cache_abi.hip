@@ -27,6 +27,9 @@ dspark_status check_cache(const dspark_cache* C) {
 
 // largest max_new: rows are counted in 31 bits, also after the heads of a group are folded in
 constexpr int32_t kMaxNew = 1 << 20;
+constexpr long long kMaxTiles = 1 << 24;
+// a window that hides nothing: positions lie in [-2^20, 2^24)
+constexpr int32_t kNoWindow = 1 << 26;
 
 // What append and attend have in common.  rows: strided arrays of `heads` heads.
 dspark_status check_tokens(const dspark_cache& C, int32_t layer, int32_t n_rows, const int32_t* n_new,
@@ -164,6 +167,8 @@ extern "C" dspark_status dspark_cache_attend(const dspark_cache* C, int32_t laye
   st = check_tokens(*C, layer, n_rows, n_new, row_start, max_new, length, table, k_pool, v_pool, k_scale, v_scale);
   if (st != DSPARK_OK) return st;
   if (!(scale > 0.0f) || !isfinite(scale) || window < 0) return DSPARK_E_INVALID;
+  // row tiles (of 16 rows or more) over which the workers look for their share
+  if ((((long long)max_new * (C->Hq / C->Hkv) + 15) / 16) * C->B > kMaxTiles) return DSPARK_E_INVALID;
   if (!aligned(lse, 4)) return DSPARK_E_POINTER;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < dspark_cache_workspace_bytes(C, max_new))
     return DSPARK_E_WORKSPACE;
@@ -187,7 +192,7 @@ extern "C" dspark_status dspark_cache_attend(const dspark_cache* C, int32_t laye
   a.v_pool = static_cast<const char*>(v_pool) + layer * layer_bytes;
   a.scale2 = (float)((double)scale * 1.4426950408889634);
   a.causal = causal != 0;
-  a.window = window;
+  a.window = window < kNoWindow ? window : kNoWindow;
   a.workspace = workspace;
   return launch_cache_attend(*C, a, stream) == hipSuccess ? DSPARK_OK : DSPARK_E_LAUNCH;
 }

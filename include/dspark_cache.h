@@ -42,9 +42,10 @@
  *
  * Supported: 1 <= B <= 65536; page in {16, 32, 64, 128, 256}; 1 <= max_pages with
  * max_pages * page <= 2^24; 1 <= n_pages <= 2^24; 1 <= n_layers <= 1024;
- * Hq a multiple of Hkv, 1 <= Hkv, Hq <= 1024; D in {64, 128, 256}.  Types (data
- * = q, k, v, out): fp32 data with an fp32 cache, bf16 data with a bf16 or an e4m3
- * cache.  Pools, q, k, v, out 16-byte aligned; other arrays 4-byte aligned.
+ * Hq a multiple of Hkv, 1 <= Hkv, Hq <= 1024; D in {64, 128, 256}; 1 <= max_new <=
+ * 2^20, for attend with B * ceil(max_new * Hq / Hkv / 16) <= 2^24.  Types (data = q,
+ * k, v, out): fp32 data with an fp32 cache, bf16 data with a bf16 or an e4m3 cache.
+ * Pools, q, k, v, out 16-byte aligned; other arrays 4-byte aligned.
  */
 #ifndef DSPARK_CACHE_H
 #define DSPARK_CACHE_H
@@ -83,8 +84,8 @@ size_t dspark_cache_workspace_bytes(const dspark_cache* C, int32_t max_new);
  * Inputs:  k, v [n_rows][Hkv][D] (data_dtype; rows k_stride and v_stride elements
  *          apart, each a multiple of 16 bytes); n_new [B] int32 or NULL (max_new
  *          everywhere); row_start [B] int32 or NULL (b * max_new); length [B];
- *          table [B][max_pages]; k_scale, v_scale [Hkv] fp32 for an e4m3 cache
- *          (ignored otherwise).
+ *          table [B][max_pages]; k_scale, v_scale [Hkv] fp32, finite and positive,
+ *          for an e4m3 cache (ignored otherwise).
  * In/out:  k_pool, v_pool: layer `layer` receives the tokens; nothing else changes.
  * An e4m3 cache stores x / scale rounded to nearest (ties to even), values past
  * +-448 as +-448, NaN as NaN.  A page that several slots hold must not be written
@@ -110,7 +111,7 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  *          scale > 0, finite.
  * Outputs: out [n_rows][Hq][D] (rows out_stride elements apart); lse
  *          [n_rows][Hq] fp32 or NULL.  Rows that belong to no request are left as
- *          they were.
+ *          they were.  Outputs must not overlap the inputs or each other.
  * Products and sums are fp32; with bf16 data the softmax weights are rounded to
  * bf16 for their product with the values.  causal = 0 is the mask of a parallel
  * drafter's block.  n_rows = 0 does nothing.

@@ -146,6 +146,14 @@ def test_e4m3_needs_its_scales(ds):
         assert c["append"]() == PTR and c["attend"]() == PTR
 
 
+def test_more_row_tiles_than_attend_serves(ds):
+    # 65536 requests x 2^20 rows x 1024 heads of a group: refused, not searched for hours
+    C = problem(ds, B=65536, Hq=1024, Hkv=1)
+    assert calls(ds, C, Memory(), max_new=1 << 20, qs=1024 * 128, os=1024 * 128)["attend"]() == INV
+    C = problem(ds, B=4096, Hq=16, Hkv=1)
+    assert calls(ds, C, Memory(), max_new=4097, qs=2048, os=2048)["attend"]() == INV
+
+
 def test_null_cache_and_no_rows(ds):
     for name, call in calls(ds, None, Memory()).items():
         assert call() == PTR, name
@@ -158,7 +166,7 @@ def test_workspace_sizes(ds):
     assert a > 0 and a % 256 == 0
     assert ds.cache_workspace_bytes(problem(ds), 0) == 0
     assert ds.cache_workspace_bytes(problem(ds), (1 << 20) + 1) == 0
-    assert ds.cache_workspace_bytes(problem(ds, n_pages=1 << 20), 1) > a
+    assert ds.cache_workspace_bytes(problem(ds, n_pages=1 << 23), 1) > a
 
 
 def test_binding_refuses_host_tensors(ds):

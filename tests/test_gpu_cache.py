@@ -117,6 +117,15 @@ def test_attend_row_counts(ds, dtype, D, page, rows, G, wide):
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_window_of_any_size(ds, causal):
+    # fewer cached tokens than rows, and windows up to the largest integer: the same as none
+    c = cu.make(31, "bf16", 16, 64, 4, 2, [9, 2], [5, 40])
+    ref = cu.oracle_attend(c, causal=causal)
+    for window in (1 << 20, 2**31 - 1):
+        check_attend(c, *gpu_attend(ds, c, causal=causal, window=window), ref)
+
+
 def test_attend_long_context(ds):
     c = cu.make(30, "bf16", 64, 64, 2, 1, [1, 2], [20000, 9], poison=False)
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
