@@ -197,9 +197,9 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _stream_of(device, stream):
+def _stream_of(index, stream):
     """Handle of `stream`, or of the device's current one (asked for without a Stream object, 3 us cheaper)."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _check(fn: str, status: int) -> None:
@@ -374,32 +374,36 @@ def cache_workspace_bytes(C: Cache, max_new: int) -> int:
     return int(load().dspark_cache_workspace_bytes(ctypes.byref(C), int(max_new)))
 
 
-def _refuse(t, dtype, shape, device, name):
+def _refuse(t, dtype, shape, index, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _dev(t, dtype, shape, device, name, optional=False):
-    """Address of a dense tensor of this dtype and shape on `device`; None passes NULL if optional."""
-    if t is None and optional:
-        return None
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device
-            or not t.is_contiguous()):
-        _refuse(t, dtype, shape, device, name)
-    return t.data_ptr()
+# The checks below are written for the cost of a call (0.3 us a tensor): one expression where all is well.
+def _dev(t, dtype, shape, index, name):
+    """Address of a dense tensor of this dtype and shape on device `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, dtype, shape, index, name)
 
 
-def _rows(t, dtype, shape, device, name):
+def _opt(t, dtype, shape, index, name):
+    """The same, or NULL for None."""
+    return None if t is None else _dev(t, dtype, shape, index, name)
+
+
+def _rows(t, dtype, shape, index, name):
     """(address, row stride) of [rows][heads][D] whose rows are dense but may lie apart."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        _refuse(t, dtype, shape, device, name)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, dtype, shape, index, name)
     s = t.stride()
     if s[2] != 1 or s[1] != shape[2]:
         raise ValueError(f"{name}'s rows must be dense")
@@ -408,20 +412,20 @@ def _rows(t, dtype, shape, device, name):
 
 def _device(t):
     """The device of the call: that of its tensors, which has to be the current one."""
-    d = t.device
-    if d.type != "cuda":
+    index = t.get_device()
+    if index < 0:
         raise ValueError("the cache's tensors must be device tensors")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {d}, the current device is cuda:{torch.cuda.current_device()}")
-    return d
+    if index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    return index
 
 
-def _workspace(t, device):
-    if t.device != device:
-        raise ValueError(f"workspace is on {t.device}, expected {device}")
+def _workspace(t, index):
+    if t.get_device() != index:
+        raise ValueError(f"workspace is on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def cache_append(C: Cache, layer: int, k, v, n_new, row_start, max_new: int, length, table, k_scale, v_scale,
@@ -433,10 +437,10 @@ def cache_append(C: Cache, layer: int, k, v, n_new, row_start, max_new: int, len
     kp, ks = _rows(k, dt, (rows, C.Hkv, C.D), dev, "k")
     vp, vs = _rows(v, dt, (rows, C.Hkv, C.D), dev, "v")
     st = lib.dspark_cache_append(
-        C, layer, kp, ks, vp, vs, rows, _dev(n_new, i32, B, dev, "n_new", True),
-        _dev(row_start, i32, B, dev, "row_start", True), max_new, _dev(length, i32, B, dev, "length"),
-        _dev(table, i32, (C.B, C.max_pages), dev, "table"), _dev(k_scale, f32, (C.Hkv,), dev, "k_scale", True),
-        _dev(v_scale, f32, (C.Hkv,), dev, "v_scale", True), _dev(k_pool, ct, C.k_shape, dev, "k_pool"),
+        C, layer, kp, ks, vp, vs, rows, _opt(n_new, i32, B, dev, "n_new"),
+        _opt(row_start, i32, B, dev, "row_start"), max_new, _dev(length, i32, B, dev, "length"),
+        _dev(table, i32, (C.B, C.max_pages), dev, "table"), _opt(k_scale, f32, (C.Hkv,), dev, "k_scale"),
+        _opt(v_scale, f32, (C.Hkv,), dev, "v_scale"), _dev(k_pool, ct, C.k_shape, dev, "k_pool"),
         _dev(v_pool, ct, C.v_shape, dev, "v_pool"), _stream_of(dev, stream))
     _check("dspark_cache_append", st)
 
@@ -452,12 +456,12 @@ def cache_attend(C: Cache, layer: int, q, n_new, row_start, max_new: int, length
     op, os_ = _rows(out, dt, (rows, C.Hq, C.D), dev, "out")
     ws, nbytes = _workspace(workspace, dev)
     st = lib.dspark_cache_attend(
-        C, layer, qp, qs, rows, _dev(n_new, i32, B, dev, "n_new", True), _dev(row_start, i32, B, dev, "row_start", True),
+        C, layer, qp, qs, rows, _opt(n_new, i32, B, dev, "n_new"), _opt(row_start, i32, B, dev, "row_start"),
         max_new, _dev(length, i32, B, dev, "length"), _dev(table, i32, (C.B, C.max_pages), dev, "table"),
         _dev(k_pool, ct, C.k_shape, dev, "k_pool"), _dev(v_pool, ct, C.v_shape, dev, "v_pool"),
-        _dev(k_scale, f32, (C.Hkv,), dev, "k_scale", True), _dev(v_scale, f32, (C.Hkv,), dev, "v_scale", True),
+        _opt(k_scale, f32, (C.Hkv,), dev, "k_scale"), _opt(v_scale, f32, (C.Hkv,), dev, "v_scale"),
         C.D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, os_,
-        _dev(lse, f32, (rows, C.Hq), dev, "lse", True), ws, nbytes, _stream_of(dev, stream))
+        _opt(lse, f32, (rows, C.Hq), dev, "lse"), ws, nbytes, _stream_of(dev, stream))
     _check("dspark_cache_attend", st)
 
 
@@ -469,7 +473,7 @@ def cache_update(C: Cache, parent, new_len, table, length, ref, table_out, lengt
     T, N = (C.B, C.max_pages), (C.n_pages,)
     ws, nbytes = _workspace(workspace, dev)
     st = lib.dspark_cache_update(
-        C, _dev(parent, i32, B, dev, "parent", True), _dev(new_len, i32, B, dev, "new_len"),
+        C, _opt(parent, i32, B, dev, "parent"), _dev(new_len, i32, B, dev, "new_len"),
         _dev(table, i32, T, dev, "table"), _dev(length, i32, B, dev, "length"), _dev(ref, i32, N, dev, "ref"),
         _dev(table_out, i32, T, dev, "table_out"), _dev(length_out, i32, B, dev, "length_out"),
         _dev(ref_out, i32, N, dev, "ref_out"), _dev(n_short, i32, (1,), dev, "n_short"),
