@@ -3,14 +3,14 @@
 //
 // Mathematics.  For a kv head, the G query heads that read it and the new tokens of
 // a request form the rows of one product: row rho = (token rho / G, head rho % G).
-// A tile of 32 keys gives S^T = K Q^T (32 keys x 32 rows) and O^T += V^T P^T with
+// A tile of keys gives S^T = K Q^T (keys x rows) and O^T += V^T P^T with
 // P = exp2(c S - m), c the softmax scale times log2(e), m the row's running maximum,
 // l the running sum of P.  Transposed, a row is one MFMA column, that is one lane and
-// its partner 32 lanes on: the maximum and the sum of a row need one lane swap, a
-// rescaling of O is one factor per lane, and the registers that S^T leaves are, once
-// exponentiated and rounded, the B operand of the second product as they stand.  The
-// last holds because the rows of K are read in an order chosen for it (key_of): the
-// product sums over keys, so their order within the tile is free.
+// its partners 32 (or 16) lanes on: the maximum and the sum of a row need one or two
+// lane swaps, a rescaling of O is one factor per lane, and the registers that S^T
+// leaves are, once exponentiated and rounded, the B operand of the second product as
+// they stand.  The last holds because the rows of K are read in an order chosen for it
+// (key_of_row): the product sums over keys, so their order within the tile is free.
 //
 // Running maximum.  m only moves when some row's maximum rises by more than 2^8 in
 // weight; until then P may reach 2^8, which costs no precision (fp32 sums, and bf16
@@ -32,7 +32,6 @@ namespace dspark {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2_t;
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kAttendThreads = 256;
 constexpr float kRescale = 8.f;  // log2 of the weight up to which the maximum may lag
@@ -273,88 +272,17 @@ __device__ __forceinline__ bf16x8_t f8_to_bf16x8(uint32_t lo, uint32_t hi) {
   __builtin_memcpy(&o, r, 16);
   return o;
 }
-__device__ __forceinline__ f32x16_t mma(bf16x8_t x, bf16x8_t y, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16_t mma(float x, float y, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x2f32(x, y, c, 0, 0, 0);
-}
-__device__ __forceinline__ float lane4(const uint4& w, int e) {
-  return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
-}
 
-// Row m of the K operand holds this key of the tile.  S^T row m = 8 j + 4 h + i sits in
-// register 4 j + i of half-wave h; the bf16 product takes 8 consecutive keys of a
-// 16-key slab from each half, so those rows are the keys 16 (j / 2) + 8 h + 4 (j % 2) + i.
-// The fp32 product takes one key of each half at a time: rows are keys.
-template <bool F32>
-__device__ __forceinline__ int key_of_row(int m) {
-  if (F32) return m;
-  const int j = m >> 3, h = (m >> 2) & 1, i = m & 3;
-  return 16 * (j >> 1) + 8 * h + 4 * (j & 1) + i;
-}
-// The key of score register r in half-wave h.
-template <bool F32>
-__device__ __forceinline__ constexpr int key_of_reg(int r, int h) {
-  return F32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 16 * (r >> 3) + 8 * h + (r & 7);
-}
-
-// A lane's part of a 32-key tile: K row (l % 32) and, for each 32 coordinates, the
-// values of its keys.  16-byte loads throughout.
-//   bf16: K register x holds d = 16 x + 8 h ..; V register (s, db) the keys 16 s + 8 h ..
-//   e4m3: K register x holds d = 32 x + 16 h ..; V (s, db) 8 bytes
-//   fp32: K register x holds d = 8 x + 4 h ..; V (j, db) the keys 8 j + 4 h ..
-template <int CT, int D>
-struct Tile {
-  static constexpr bool kF32 = CT == DSPARK_F32;
-  static constexpr int kK = CT == DSPARK_F32 ? D / 8 : CT == DSPARK_BF16 ? D / 16 : D / 32;  // uint4
-  static constexpr int kSlabs = kF32 ? 4 : 2;
-  static constexpr int kBlocks = D / 32;
-  using V = typename std::conditional<CT == DSPARK_F8E4M3, uint2, uint4>::type;
-};
-
-// The first coordinate that half h of Q (and K) register x holds; of 8 (bf16 operand)
-// or 4 (fp32) consecutive ones.
-template <int CT>
-__device__ __forceinline__ constexpr int coord(int x, int h) {
-  return CT == DSPARK_F32 ? 8 * x + 4 * h : CT == DSPARK_BF16 ? 16 * x + 8 * h : 32 * (x >> 1) + 16 * h + 8 * (x & 1);
-}
-template <int CT, int D>
-constexpr int q_regs() { return CT == DSPARK_F32 ? D / 8 : D / 16; }
-
-// S^T of one 32-row block
-template <int CT, int D>
-__device__ __forceinline__ f32x16_t scores(const uint4 (&k)[Tile<CT, D>::kK], const uint4 (&q)[q_regs<CT, D>()]) {
-  f32x16_t s = {};
-#pragma unroll
-  for (int x = 0; x < Tile<CT, D>::kK; ++x) {
-    if constexpr (CT == DSPARK_F32) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s = mma(lane4(k[x], e), lane4(q[x], e), s);
-    } else if constexpr (CT == DSPARK_BF16) {
-      s = mma(as_bf16x8(k[x]), as_bf16x8(q[x]), s);
-    } else {
-      s = mma(f8_to_bf16x8(k[x].x, k[x].y), as_bf16x8(q[2 * x]), s);
-      s = mma(f8_to_bf16x8(k[x].z, k[x].w), as_bf16x8(q[2 * x + 1]), s);
-    }
-  }
-  return s;
-}
-
-// One row's running state in a lane: m is common to the row's two lanes, l is the
-// lane's share of the sum.
+// One row's running state in a lane: m is common to the row's lanes, l is the lane's
+// share of the sum.
 struct Running {
   float m, l;
 };
 
-// Leaves the scores of the tile's keys that the row sees (lo <= key < hi).  The half's
-// offset goes into the bounds, so that a key is a constant.
-template <bool F32>
-__device__ __forceinline__ void mask_scores(f32x16_t& s, int lo, int hi, int h) {
-  const int from = lo - (F32 ? 4 : 8) * h;
-  const unsigned n = max(0, hi - lo);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = (unsigned)(key_of_reg<F32>(i, 0) - from) < n ? s[i] : -INFINITY;
+// From scores to exponents of 2.  Not 0, so that a score of -inf stays one.
+template <int CT>
+__device__ __forceinline__ float score_factor(const AttendArgs& a, int head) {
+  return fmaxf(CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2, 0x1p-126f);
 }
 
 // The running maximum moves to include `top`; returns the factor by which O and l fade.
@@ -364,44 +292,6 @@ __device__ __forceinline__ float fade_to(Running& r, float top) {
   r.m = m;
   r.l *= fade;
   return fade;
-}
-
-// The running maximum over N score tiles of a row; returns the factor by which O and l
-// fade (1 for most tiles).
-template <int N>
-__device__ __forceinline__ float raise_max(const f32x16_t (&s)[N], Running& r, float c) {
-  float top = s[0][0];
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
-  top = halves32_max(top) * c;
-  if (!__any(top > r.m + kRescale)) return 1.f;
-  return fade_to(r, top);
-}
-// Scores to weights; l grows by their sum.
-__device__ __forceinline__ void weights(f32x16_t& s, Running& r, float c) {
-  const float ref = r.m == -INFINITY ? 0.f : r.m;
-  float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
-    s[i + 1] = __builtin_amdgcn_exp2f(fmaf(s[i + 1], c, -ref));
-    sum0 += s[i];
-    sum1 += s[i + 1];
-  }
-  r.l += sum0 + sum1;
-}
-
-__device__ __forceinline__ bf16x8_t pack8(const f32x16_t& s, int at) {
-  bf16x8_t o;
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const bf16x2_t p = __builtin_convertvector(f32x2_t{s[at + i], s[at + i + 1]}, bf16x2_t);
-    o[i] = p[0];
-    o[i + 1] = p[1];
-  }
-  return o;
 }
 
 // ---- values that a tile's rows see in part or not at all
@@ -450,40 +340,10 @@ __device__ __forceinline__ bf16x8_t value_operand(const V& v) {
     return f8_to_bf16x8(v.x, v.y);
 }
 
-// O^T += V^T P^T of one 32-row block
-template <int CT, int D>
-__device__ __forceinline__ void add_values(const typename Tile<CT, D>::V (&v)[Tile<CT, D>::kSlabs][D / 32],
-                                           const f32x16_t& w, f32x16_t (&acc)[D / 32]) {
-  if constexpr (CT == DSPARK_F32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int db = 0; db < D / 32; ++db) acc[db] = mma(lane4(v[j][db], e), w[4 * j + e], acc[db]);
-  } else {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const bf16x8_t p = pack8(w, 8 * s);
-#pragma unroll
-      for (int db = 0; db < D / 32; ++db) acc[db] = mma(value_operand<CT>(v[s][db]), p, acc[db]);
-    }
-  }
-}
-
 // ---- results
 // out and lse of one row from its sums
 __device__ __forceinline__ float row_factor(float l, float vs) { return l == 0.f ? 0.f : vs / l; }
 
-template <int CT>
-__device__ __forceinline__ float4 load4(const void* out, size_t at) {
-  if constexpr (CT == DSPARK_F32) {
-    return *reinterpret_cast<const float4*>(static_cast<const float*>(out) + at);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(out) + at);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-  }
-}
 template <int CT>
 __device__ __forceinline__ void store4(void* out, size_t at, float4 y) {
   if constexpr (CT == DSPARK_F32) {

@@ -21,6 +21,9 @@ namespace dspark {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
+__device__ __forceinline__ float lane4(const uint4& w, int e) {
+  return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
+}
 __device__ __forceinline__ f32x4_t mma16(bf16x8_t x, bf16x8_t y, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
 }
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
       for (int x = 0; x < TT::kQ; ++x)
         q[nb][x] = make_uint4(q[nb][x].x & there, q[nb][x].y & there, q[nb][x].z & there, q[nb][x].w & there);
     }
-    const float ks = CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2;
+    const float ks = score_factor<CT>(a, head);
     __syncthreads();
 
     for (; key0 <= last; key0 += 128) {

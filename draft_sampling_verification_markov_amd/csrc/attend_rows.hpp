@@ -20,6 +20,83 @@
 
 namespace dspark {
 
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16_t mma(bf16x8_t x, bf16x8_t y, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+}
+
+// Row m of the K operand holds this key of the tile.  S^T row m = 8 j + 4 h + i sits in
+// register 4 j + i of half-wave h; the product with the values takes 8 consecutive keys
+// of a 16-key slab from each half, so those rows are the keys
+// 16 (j / 2) + 8 h + 4 (j % 2) + i.
+__device__ __forceinline__ int key_of_row(int m) {
+  const int j = m >> 3, h = (m >> 2) & 1, i = m & 3;
+  return 16 * (j >> 1) + 8 * h + 4 * (j & 1) + i;
+}
+// The key of score register r in half-wave 0; half-wave 1 holds the key 8 on.
+__device__ __forceinline__ constexpr int key_of_reg(int r) { return 16 * (r >> 3) + (r & 7); }
+
+// The first of the 8 consecutive coordinates that half h of Q register x holds: where
+// K's pieces of 16 bytes (e4m3: of 16 coordinates) have them.
+template <int CT>
+__device__ __forceinline__ constexpr int coord(int x, int h) {
+  return CT == DSPARK_BF16 ? 16 * x + 8 * h : 32 * (x >> 1) + 16 * h + 8 * (x & 1);
+}
+
+// Leaves the scores of the tile's keys that the row sees (lo <= key < hi).  The half's
+// offset goes into the bounds, so that a key is a constant.
+__device__ __forceinline__ void mask_scores(f32x16_t& s, int lo, int hi, int h) {
+  const int from = lo - 8 * h;
+  const unsigned n = max(0, hi - lo);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = (unsigned)(key_of_reg(i) - from) < n ? s[i] : -INFINITY;
+}
+
+// The running maximum over N score tiles of a row; returns the factor by which O and l
+// fade (1 for most tiles).
+template <int N>
+__device__ __forceinline__ float raise_max(const f32x16_t (&s)[N], Running& r, float c) {
+  float top = s[0][0];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
+  top = halves32_max(top) * c;
+  if (!__any(top > r.m + kRescale)) return 1.f;
+  return fade_to(r, top);
+}
+// Scores to weights; l grows by their sum.
+__device__ __forceinline__ void weights(f32x16_t& s, Running& r, float c) {
+  const float ref = r.m == -INFINITY ? 0.f : r.m;
+  float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
+    s[i + 1] = __builtin_amdgcn_exp2f(fmaf(s[i + 1], c, -ref));
+    sum0 += s[i];
+    sum1 += s[i + 1];
+  }
+  r.l += sum0 + sum1;
+}
+
+__device__ __forceinline__ bf16x8_t pack8(const f32x16_t& s, int at) {
+  bf16x8_t o;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const bf16x2_t p = __builtin_convertvector(f32x2_t{s[at + i], s[at + i + 1]}, bf16x2_t);
+    o[i] = p[0];
+    o[i + 1] = p[1];
+  }
+  return o;
+}
+
+// four bf16 values of a result that this lane stored
+__device__ __forceinline__ float4 load4(const void* out, size_t at) {
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(out) + at);
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+
 template <int CT, int D>
 struct RowsShape {
   static constexpr int kEs = Operand<CT>::kBytes;
@@ -31,6 +108,9 @@ struct RowsShape {
   static constexpr int kOps = kBytes / 1024 / 4;               // DMA instructions a wave, keys (or values)
   static constexpr int kPerCu = 2;                           // workgroups that a CU holds
   static constexpr int kAhead = D == 256 ? 3 : 4;            // LDS reads before their products (more spill at 256)
+  static constexpr int kQ = D / 16;                          // registers of Q (16 bytes a lane)
+  static constexpr int kBlocks = D / 32;                     // of 32 coordinates
+  using V = typename std::conditional<CT == DSPARK_F8E4M3, uint2, uint4>::type;  // 8 tokens of a coordinate
   // 64 banks of 4 bytes: 16 pieces a cycle, one or more rows of keys
   __device__ __forceinline__ static int swizzle(int r) { return kPieces >= 16 ? r & 15 : (r / (16 / kPieces)) & (kPieces - 1); }
 };
@@ -54,8 +134,7 @@ __device__ __forceinline__ void dma_1k(__amdgpu_buffer_rsrc_t src, int offset, u
 template <int CT, int D, bool ONCE>
 __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_rows(AttendArgs a, Split p) {
   using S = RowsShape<CT, D>;
-  using TT = Tile<CT, D>;
-  constexpr int kQ = q_regs<CT, D>(), kRows = S::kRows, kEs = S::kEs;
+  constexpr int kQ = S::kQ, kRows = S::kRows, kEs = S::kEs;
   constexpr int kOps = S::kOps;
   constexpr int kWavesPerSub16 = 4 / (S::kKeys / 16);  // waves that share the DMA of 16 keys
   __shared__ __attribute__((aligned(1024))) unsigned char k0[S::kBytes], k1[S::kBytes], v0[S::kBytes], v1[S::kBytes];
@@ -93,7 +172,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
   for (int i = 0; i < kOps; ++i) {
     const int at = (wave * kOps + i) * 64 + lane;  // piece of the tile's keys
     const int r = at / S::kPieces, piece = (at % S::kPieces) ^ S::swizzle(r);
-    k_src[i] = (key_of_row<false>(r & 31) & 15) * (D * kEs) + piece * 16;
+    k_src[i] = (key_of_row(r & 31) & 15) * (D * kEs) + piece * 16;
   }
   v_src = ((wave * kOps * 64 + lane) % (S::kPieces * 16)) * 16;
   // reading: this lane's K row is col of each half tile, pieces 2 x + h, at k_at ^ 32 x
@@ -120,11 +199,11 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     uint4 q[kQ];
     int row_lo = 0, row_hi = 0x7fffffff;  // a column without a row sees everything and is left out at the end
     Running run{-INFINITY, 0.f};
-    f32x16_t acc[TT::kBlocks];
+    f32x16_t acc[S::kBlocks];
     const int rho = wrow + col;
     {
 #pragma unroll
-      for (int db = 0; db < TT::kBlocks; ++db) acc[db] = f32x16_t{};
+      for (int db = 0; db < S::kBlocks; ++db) acc[db] = f32x16_t{};
       int hq = 0;
       long long r = -1;
       if (rho < g.rows) {
@@ -141,7 +220,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       for (int x = 0; x < kQ; ++x)
         q[x] = make_uint4(q[x].x & there, q[x].y & there, q[x].z & there, q[x].w & there);
     }
-    const float ks = CT == DSPARK_F8E4M3 ? a.scale2 * a.k_scale[head] : a.scale2;
+    const float ks = score_factor<CT>(a, head);
 
     // the 16 keys (or values) of tile t that this wave brings, as a buffer
     auto source = [&](const void* pool, int raw, int t) __attribute__((always_inline)) {
@@ -159,8 +238,8 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       unsigned char* const at = to + wave * kOps * 1024;
       dma_1k<0, ONCE>(src, v_src, at);
       if constexpr (kOps > 1) dma_1k<1024, ONCE>(src, v_src, at);
-      if constexpr (kOps > 2) dma_1k<2048, ONCE>(src, v_src, at);
-      if constexpr (kOps > 3) dma_1k<3072, ONCE>(src, v_src, at);
+      if constexpr (kOps > 2) dma_1k<2 * 1024, ONCE>(src, v_src, at);
+      if constexpr (kOps > 3) dma_1k<3 * 1024, ONCE>(src, v_src, at);
     };
     auto raw_id = [&](int t) __attribute__((always_inline)) { return row.raw(min(t, t1 - 1) * S::kKeys + 16 * sub16); };
 
@@ -169,7 +248,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       int at = k_at;
       if (D == 256) asm volatile("" : "+v"(at));  // no room for 16 addresses kept from tile to tile
 #pragma unroll
-      for (int x = 0; x < TT::kK; ++x) {
+      for (int x = 0; x < S::kPieces / 2; ++x) {
         const uint4 k = *reinterpret_cast<const uint4*>(kb + sub * 32 * (D * kEs) + (at ^ (32 * x)));
         if constexpr (CT == DSPARK_BF16) {
           w = mma(as_bf16x8(k), as_bf16x8(q[x]), w);
@@ -181,7 +260,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     };
     auto value = [&](const unsigned char* vb, int sub, int sl, int db) __attribute__((always_inline)) {
       return value_operand<CT>(
-          *reinterpret_cast<const typename TT::V*>(vb + ((sub * 4 + 2 * sl + h) * D + 32 * db + col) * (8 * kEs)));
+          *reinterpret_cast<const typename S::V*>(vb + ((sub * 4 + 2 * sl + h) * D + 32 * db + col) * (8 * kEs)));
     };
     // Waits until at most the youngest two of this wave's DMA groups (of keys or of values)
     // are on their way.  Past the last tile the last one is brought again, so that there
@@ -201,7 +280,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
 #pragma unroll
         for (int sub = 0; sub < S::kSubs; ++sub) scores(kb, sub, w[sub]);
         // LDS reads run kAhead fragments before their products
-        constexpr int kReads = S::kSubs * TT::kK, kMma = CT == DSPARK_BF16 ? 1 : 2;
+        constexpr int kReads = S::kSubs * S::kPieces / 2, kMma = CT == DSPARK_BF16 ? 1 : 2;
         schedule<kLdsRead, S::kAhead>();
 #pragma unroll
         for (int i = 0; i < kReads - S::kAhead; ++i) {
@@ -212,12 +291,12 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
         if (key0 < all_lo || key0 + S::kKeys > all_hi) {
 #pragma unroll
           for (int sub = 0; sub < S::kSubs; ++sub)
-            mask_scores<false>(w[sub], row_lo - (key0 + 32 * sub), row_hi - (key0 + 32 * sub), h);
+            mask_scores(w[sub], row_lo - (key0 + 32 * sub), row_hi - (key0 + 32 * sub), h);
         }
         const float fade = raise_max(w, run, ks);
         if (__any(fade != 1.f)) {
 #pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db) acc[db] *= fade;
+          for (int db = 0; db < S::kBlocks; ++db) acc[db] *= fade;
         }
       }
       landed();            // this wave's part of the values
@@ -247,10 +326,10 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
         for (int sl = 0; sl < 2; ++sl) {
           const bf16x8_t pw = pack8(w[sub], 8 * sl);
 #pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db) acc[db] = mma(value(vb, sub, sl, db), pw, acc[db]);
+          for (int db = 0; db < S::kBlocks; ++db) acc[db] = mma(value(vb, sub, sl, db), pw, acc[db]);
         }
       }
-      constexpr int kValues = 2 * TT::kBlocks, kSoft = 58;
+      constexpr int kValues = 2 * S::kBlocks, kSoft = 58;
       schedule<kLdsRead, S::kAhead>();
       schedule<kValu, kSoft>();
 #pragma unroll
@@ -293,7 +372,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       const float f = whole ? row_factor(l, vs) : 1.f;
       const bool none = whole && l == 0.f;
 #pragma unroll
-      for (int db = 0; db < TT::kBlocks; ++db)
+      for (int db = 0; db < S::kBlocks; ++db)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float4 y = make_float4(acc[db][4 * j] * f, acc[db][4 * j + 1] * f, acc[db][4 * j + 2] * f,
@@ -314,7 +393,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
           const size_t at = whole ? r * a.out_stride + (size_t)hq * D + d : 0;
           float4* const part = reinterpret_cast<float4*>(slot + (size_t)rho * D + d);
           if (whole && r < 0) continue;
-          const float4 x = whole ? load4<CT>(a.out, at) : *part;
+          const float4 x = whole ? load4(a.out, at) : *part;
           y = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
           if (whole)
             store4<CT>(a.out, at, y);

@@ -166,7 +166,8 @@ extern "C" dspark_status dspark_cache_attend(const dspark_cache* C, int32_t laye
   if (st != DSPARK_OK) return st;
   st = check_tokens(*C, layer, n_rows, n_new, row_start, max_new, length, table, k_pool, v_pool, k_scale, v_scale);
   if (st != DSPARK_OK) return st;
-  if (!(scale > 0.0f) || !isfinite(scale) || window < 0) return DSPARK_E_INVALID;
+  const float scale2 = (float)((double)scale * 1.4426950408889634);  // times log2(e)
+  if (!(scale > 0.0f) || !isfinite(scale2) || window < 0) return DSPARK_E_INVALID;
   // row tiles (of 16 rows or more) over which the workers look for their share
   if ((((long long)max_new * (C->Hq / C->Hkv) + 15) / 16) * C->B > kMaxTiles) return DSPARK_E_INVALID;
   if (!aligned(lse, 4)) return DSPARK_E_POINTER;
@@ -190,7 +191,7 @@ extern "C" dspark_status dspark_cache_attend(const dspark_cache* C, int32_t laye
   a.v_scale = v_scale;
   a.k_pool = static_cast<const char*>(k_pool) + layer * layer_bytes;
   a.v_pool = static_cast<const char*>(v_pool) + layer * layer_bytes;
-  a.scale2 = (float)((double)scale * 1.4426950408889634);
+  a.scale2 = scale2;
   a.causal = causal != 0;
   a.window = window < kNoWindow ? window : kNoWindow;
   a.workspace = workspace;

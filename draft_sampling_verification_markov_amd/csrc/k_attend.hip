@@ -7,11 +7,6 @@
 namespace dspark {
 namespace {
 
-struct Plan {
-  Split split;
-  int rows;  // of a tile
-};
-
 int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / C.Hkv); }
 
 // Whole segments or dealt units, for a kernel of which the chip holds `slots` workgroups.
@@ -20,16 +15,15 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // Whole are: segments of few keys, where there is nothing to share out; and `whole` or
 // more times as many as the slots.
 constexpr int kFewKeys = 1024, kWholeKeys = 16, kWholeRows = 1;
-Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int slots, int whole) {
-  Plan pl{};
-  pl.rows = rows;
-  pl.split.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
-  pl.split.unit_shift = unit_shift;
+Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int slots, int whole) {
+  Split pl{};
+  pl.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
+  pl.unit_shift = unit_shift;
   long long keys = (long long)C.max_pages * C.page;
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
-  const long long segments = (long long)C.B * pl.split.row_tiles * C.Hkv;
+  const long long segments = (long long)C.B * pl.row_tiles * C.Hkv;
   const bool direct = segments <= (1 << 22) && (keys <= kFewKeys || segments >= (long long)whole * slots);
-  pl.split.workers = direct ? 0 : slots;
+  pl.workers = direct ? 0 : slots;
   return pl;
 }
 
@@ -37,24 +31,24 @@ Plan plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int 
 // the next call, are read with the streaming policy: 256 requests x 17 rows 205 -> 192 us,
 // 256 x 1 421 -> 402.  For others it costs: prompts, whose row tiles meet in L2, 567 -> 603,
 // 72 MB of keys 28 -> 33.
-bool read_once(const dspark_cache& C, const Plan& pl) {
-  return pl.split.row_tiles == 1 && 2 * page_bytes(C) * C.n_pages > ((size_t)256 << 20);
+bool read_once(const dspark_cache& C, const Split& pl) {
+  return pl.row_tiles == 1 && 2 * page_bytes(C) * C.n_pages > ((size_t)256 << 20);
 }
 
 template <int CT, int D, int ROWS, typename Kernel>
-hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, const Plan& pl, Kernel kernel, hipStream_t s) {
-  if (!pl.split.workers) {
-    kernel<<<whole_grid(C, pl.split), kAttendThreads, 0, s>>>(a, pl.split);
+hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, const Split& pl, Kernel kernel, hipStream_t s) {
+  if (!pl.workers) {
+    kernel<<<whole_grid(C, pl), kAttendThreads, 0, s>>>(a, pl);
     return hipGetLastError();
   }
-  kernel<<<pl.split.workers, kAttendThreads, 0, s>>>(a, pl.split);
-  k_attend_join<CT, D, ROWS><<<dim3(pl.split.workers, join_groups(ROWS)), kAttendThreads, 0, s>>>(a, pl.split);
+  kernel<<<pl.workers, kAttendThreads, 0, s>>>(a, pl);
+  k_attend_join<CT, D, ROWS><<<dim3(pl.workers, join_groups(ROWS)), kAttendThreads, 0, s>>>(a, pl);
   return hipGetLastError();
 }
 
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  const Plan pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys);
+  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys);
   return run_plan<CT, D, NB * 16>(
       C, a, pl, read_once(C, pl) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
@@ -62,7 +56,7 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 template <int CT, int D>
 hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   using S = RowsShape<CT, D>;
-  const Plan pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows);
+  const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows);
   return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 

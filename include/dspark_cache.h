@@ -108,7 +108,7 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  *
  * Inputs:  q [n_rows][Hq][D] (data_dtype, rows q_stride elements apart, a multiple
  *          of 16 bytes); n_new, row_start, length, table, k_scale, v_scale as above;
- *          scale > 0, finite.
+ *          scale > 0, scale * log2(e) finite.
  * Outputs: out [n_rows][Hq][D] (rows out_stride elements apart); lse
  *          [n_rows][Hq] fp32 or NULL.  Rows that belong to no request are left as
  *          they were.  Outputs must not overlap the inputs or each other.

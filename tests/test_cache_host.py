@@ -112,7 +112,7 @@ REFUSED = [
     ("append", dict(k=None), PTR), ("append", dict(v=(1 << 41) + 4), PTR), ("append", dict(ks=255), INV),
     ("append", dict(vs=260), INV), ("append", dict(ks=248), INV), ("attend", dict(qs=1000), INV),
     ("attend", dict(q=None), PTR), ("attend", dict(out=None), PTR), ("attend", dict(os=8), INV),
-    ("attend", dict(scale=0.0), INV), ("attend", dict(scale=-1.0), INV), ("attend", dict(scale=float("inf")), INV),
+    ("attend", dict(scale=0.0), INV), ("attend", dict(scale=-1.0), INV), ("attend", dict(scale=float("inf")), INV), ("attend", dict(scale=3e38), INV),
     ("attend", dict(scale=float("nan")), INV), ("attend", dict(window=-1), INV), ("attend", dict(lse=(1 << 41) + 1), PTR),
     ("attend update compact", dict(ws=None), WSP), ("attend update compact", dict(ws=(1 << 41) + 128), WSP),
     ("attend update compact", dict(wb=64), WSP), ("update", dict(new_len=None), PTR),

@@ -126,6 +126,17 @@ def test_attend_window_of_any_size(ds, causal):
         check_attend(c, *gpu_attend(ds, c, causal=causal, window=window), ref)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "f8"])
+@pytest.mark.parametrize("G", [2, 20])
+def test_attend_scale_of_almost_nothing(ds, dtype, G):
+    # the smallest softmax scale (with an e4m3 key scale its product is 0 in fp32): what a row sees weighs the same,
+    # what it does not see still nothing
+    c = cu.make(32, dtype, 16, 64, 2 * G, 2, [3, 1], [37, 5])
+    c.k_scale.fill_(1e-3)
+    scale = float(np.float32(1e-45))
+    check_attend(c, *gpu_attend(ds, c, scale=scale), cu.oracle_attend(c, scale=scale))
+
+
 def test_attend_long_context(ds):
     c = cu.make(30, "bf16", 64, 64, 2, 1, [1, 2], [20000, 9], poison=False)
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
