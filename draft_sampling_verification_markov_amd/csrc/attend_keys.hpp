@@ -8,11 +8,13 @@
 // registers of O and Q, so that more waves are in flight, and half of the softmax's
 // work on rows that are not there.  At a segment's end the waves' sums meet in LDS.
 //
-// Tiles of 32 keys are two S^T tiles of 16 keys x 16 rows.  With lane l = 16 g + c
-// (c < 16): S^T register (t, i) holds row (of Q) c, key row 4 g + i of S tile t.  The
-// bf16 product with the values takes 8 consecutive keys of each g, so K row m of tile t
-// is read from key 8 (m / 4) + 4 t + m % 4; the fp32 product takes one key of each g at
-// a time, and K row m of tile t is key 16 t + m.
+// A tile of keys is two S^T tiles of 16 keys x 16 rows, for fp32 one (two need twice the
+// registers of K and V: 64 tokens over 4000 keys, head size 128, 148 -> 106 us; head size
+// 256, where they spill, a few hundred keys 37 -> 21).  With lane l = 16 g + c (c < 16):
+// S^T register (t, i) holds row (of Q) c, key row 4 g + i of S tile t.  The bf16 product
+// with the values takes 8 consecutive keys of each g, so K row m of tile t is read from
+// key 8 (m / 4) + 4 t + m % 4; the fp32 product takes one key of each g at a time, 4 g + i
+// for i = 0 .. 3, and K row m is key m.
 #pragma once
 
 #include "attend_core.hpp"
@@ -37,7 +39,8 @@ struct KeysTile {
   static constexpr int kEs = Operand<CT>::kBytes;
   static constexpr int kK = D * kEs / 64;  // 16-byte loads of a K row's part in a lane
   static constexpr int kQ = kF32 ? D / 16 : D / 32;
-  static constexpr int kV = kF32 ? 2 : 1;  // loads of a lane's keys of one coordinate
+  static constexpr int kS = kF32 ? 1 : 2;  // S^T tiles of 16 keys
+  static constexpr int kKeys = 16 * kS;
   static constexpr int kBlocks = D / 16;
   using V = typename std::conditional<CT == DSPARK_F8E4M3, uint2, uint4>::type;
   // first coordinate of Q register x in lane group g: where K's load has it
@@ -45,11 +48,11 @@ struct KeysTile {
     return kF32 ? 16 * x + 4 * g : CT == DSPARK_BF16 ? 32 * x + 8 * g : 64 * (x >> 1) + 16 * g + 8 * (x & 1);
   }
   __device__ __forceinline__ static int key_of_row(int t, int m) {
-    return kF32 ? 16 * t + m : 8 * (m >> 2) + 4 * t + (m & 3);
+    return kF32 ? m : 8 * (m >> 2) + 4 * t + (m & 3);
   }
-  // key of S register (t, i) in lane group 0; group g adds group_keys * g
+  // key of S register (t, i) in lane group 0; group g adds kGroupKeys * g
   static constexpr int kGroupKeys = kF32 ? 4 : 8;
-  __device__ __forceinline__ static constexpr int key_of_reg(int t, int i) { return kF32 ? 16 * t + i : 4 * t + i; }
+  __device__ __forceinline__ static constexpr int key_of_reg(int t, int i) { return 4 * t + i; }
 };
 
 // A load of keys or values; ONCE: with the streaming policy.
@@ -112,33 +115,34 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     // Page ids come over the scalar cache two tiles ahead, keys one tile ahead; past the
     // last tile the last one is loaded again, so that the loop has no branch that would
     // make the waits for its loads inexact.
-    int key0 = (t0 << 7) + 32 * wave, last = ((t1 - 1) << 7) + 32 * wave;
-    if (key0 + 32 <= g.lo) key0 += 128;
-    while (last >= g.hi && last >= key0) last -= 128;
+    constexpr int kTurn = 4 * TT::kKeys;  // keys that the four waves take
+    int key0 = (t0 << 7) + TT::kKeys * wave, last = (t1 << 7) - kTurn + TT::kKeys * wave;
+    while (key0 + TT::kKeys <= g.lo && key0 <= last) key0 += kTurn;
+    while (last >= g.hi && last >= key0) last -= kTurn;
     const int off_mask = (1 << c.page_shift) - 1;
     const char* const kp = static_cast<const char*>(a.k_pool);
     const char* const vp = static_cast<const char*>(a.v_pool);
     const TableRow row(c, g.b);
-    struct Ids { int a, b; };  // of the tile's two halves of 16 keys
-    auto ids_of = [&](int key) __attribute__((always_inline)) { return Ids{row.raw(key), row.raw(key + 16)}; };
+    struct Ids { int a, b; };  // of each 16 keys of the tile
+    auto ids_of = [&](int key) __attribute__((always_inline)) { return Ids{row.raw(key), TT::kS == 2 ? row.raw(key + 16) : 0}; };
     auto token = [&](int id, int key) __attribute__((always_inline)) {  // first byte of 16 consecutive tokens
       return (((size_t)(row.id(id) * (unsigned)c.Hkv + head) << c.page_shift) + (key & off_mask)) * (D * kEs);
     };
-    auto load_k = [&](int key0_, Ids id, uint4(&k)[2][TT::kK]) __attribute__((always_inline)) {
+    auto load_k = [&](int key0_, Ids id, uint4(&k)[TT::kS][TT::kK]) __attribute__((always_inline)) {
       const size_t half[2] = {token(id.a, key0_), token(id.b, key0_ + 16)};
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TT::kS; ++t) {
         const int key = TT::key_of_row(t, col);
-        const char* src = kp + (kF32 ? half[t] : (col < 8 ? half[0] : half[1])) + (key & 15) * (D * kEs) + 16 * g16;
+        const char* src = kp + (kF32 || col < 8 ? half[0] : half[1]) + (key & 15) * (D * kEs) + 16 * g16;
 #pragma unroll
         for (int x = 0; x < TT::kK; ++x) k[t][x] = load_key<uint4, ONCE>(src + 64 * x);
       }
     };
-    uint4 k[2][TT::kK];
+    uint4 k[TT::kS][TT::kK];
     Ids id0{}, id1{};
     if (key0 <= last) {
       id0 = ids_of(key0);
-      id1 = ids_of(min(key0 + 128, last));
+      id1 = ids_of(min(key0 + kTurn, last));
       load_k(key0, id0, k);
     }
 
@@ -178,28 +182,23 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     const float ks = score_factor<CT>(a, head);
     __syncthreads();
 
-    for (; key0 <= last; key0 += 128) {
-      const int next = min(key0 + 128, last);
-      const Ids id2 = ids_of(min(key0 + 256, last));
-      typename TT::V v[TT::kV][TT::kBlocks];
+    for (; key0 <= last; key0 += kTurn) {
+      const int next = min(key0 + kTurn, last);
+      const Ids id2 = ids_of(min(key0 + 2 * kTurn, last));
+      typename TT::V v[TT::kBlocks];
       {
-        // bf16, e4m3: the lane's 8 keys are group g16 of the tile; fp32: of S tile t, group
-        // 2 t + g16 / 2, the half g16 % 2
+        // the lane's 8 (fp32: 4) keys of coordinate 16 db + col
         const size_t half[2] = {token(id0.a, key0), token(id0.b, key0 + 16)};
+        const char* src = kF32 ? vp + half[0] + ((g16 >> 1) * D + col) * 32 + 16 * (g16 & 1)
+                               : vp + (g16 < 2 ? half[0] : half[1]) + ((g16 & 1) * D + col) * (8 * kEs);
 #pragma unroll
-        for (int t = 0; t < TT::kV; ++t) {
-          const char* src = kF32 ? vp + half[t] + ((g16 >> 1) * D + col) * 32 + 16 * (g16 & 1)
-                                 : vp + (g16 < 2 ? half[0] : half[1]) + ((g16 & 1) * D + col) * (8 * kEs);
-#pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db)
-            v[t][db] = load_key<typename TT::V, ONCE>(src + db * (16 * 8 * kEs));
-        }
+        for (int db = 0; db < TT::kBlocks; ++db) v[db] = load_key<typename TT::V, ONCE>(src + db * (16 * 8 * kEs));
       }
-      f32x4_t w[NB][2];
+      f32x4_t w[NB][TT::kS];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < TT::kS; ++t) {
           w[nb][t] = f32x4_t{};
           if (nb < blocks) {
 #pragma unroll
@@ -219,28 +218,24 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
       load_k(next, id1, k);
       id0 = id1;
       id1 = id2;
-      if (key0 < g.all_lo || key0 + 32 > g.all_hi) {  // not every row sees the whole tile
+      if (key0 < g.all_lo || key0 + TT::kKeys > g.all_hi) {  // not every row sees the whole tile
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int from = row_lo[nb] - key0 - TT::kGroupKeys * g16;
           const unsigned n = max(0, row_hi[nb] - row_lo[nb]);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < TT::kS; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               w[nb][t][i] = (unsigned)(TT::key_of_reg(t, i) - from) < n ? w[nb][t][i] : -INFINITY;
         }
         uint32_t bits = 0;
 #pragma unroll
-        for (int t = 0; t < TT::kV; ++t)
-#pragma unroll
-          for (int db = 0; db < TT::kBlocks; ++db) find_nonfinite<CT>(v[t][db], bits);
+        for (int db = 0; db < TT::kBlocks; ++db) find_nonfinite<CT>(v[db], bits);
         if (__any(bits & kOdd<CT>)) {
           odd = 1;
 #pragma unroll
-          for (int t = 0; t < TT::kV; ++t)
-#pragma unroll
-            for (int db = 0; db < TT::kBlocks; ++db) v[t][db] = finite_part<CT>(v[t][db]);
+          for (int db = 0; db < TT::kBlocks; ++db) v[db] = finite_part<CT>(v[db]);
         }
       }
 #pragma unroll
@@ -248,7 +243,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
         if (nb < blocks) {
           float top = w[nb][0][0];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < TT::kS; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = fmaxf(top, w[nb][t][i]);
           top = groups_max(top) * ks;
@@ -260,7 +255,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
           const float ref = run[nb].m == -INFINITY ? 0.f : run[nb].m;
           float sum = 0.f;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < TT::kS; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               w[nb][t][i] = __builtin_amdgcn_exp2f(fmaf(w[nb][t][i], ks, -ref));
@@ -269,16 +264,14 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
           run[nb].l += sum;
           if constexpr (kF32) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int db = 0; db < TT::kBlocks; ++db)
-                  acc[nb][db] = mma16(lane4(v[t][db], e), w[nb][t][e], acc[nb][db]);
+              for (int db = 0; db < TT::kBlocks; ++db)
+                acc[nb][db] = mma16(lane4(v[db], e), w[nb][0][e], acc[nb][db]);
           } else {
             bf16x8_t pw;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < TT::kS; ++t)
 #pragma unroll
               for (int i = 0; i < 4; i += 2) {
                 const bf16x2_t x = __builtin_convertvector(f32x2_t{w[nb][t][i], w[nb][t][i + 1]}, bf16x2_t);
@@ -287,7 +280,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
               }
 #pragma unroll
             for (int db = 0; db < TT::kBlocks; ++db)
-              acc[nb][db] = mma16(value_operand<CT>(v[0][db]), pw, acc[nb][db]);
+              acc[nb][db] = mma16(value_operand<CT>(v[db]), pw, acc[nb][db]);
           }
         }
     }
@@ -326,7 +319,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
                                  o0.w + o1.w + o2.w + o3.w);
           if (odd) {
             const int pos = g.pos0 + (g.row0 + rho) / G;
-            add_nonfinite<CT, D, 32>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
+            add_nonfinite<CT, D, TT::kKeys>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
           }
           if (whole) {
             int hq;

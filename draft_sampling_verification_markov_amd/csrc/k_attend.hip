@@ -12,17 +12,18 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // Whole segments or dealt units, for a kernel of which the chip holds `slots` workgroups.
 // Whole segments need no partial results, and the row tiles of a head run side by side
 // through one L2; but they leave the chip idle where they are few or of unequal length.
-// Whole are: segments of few keys, where there is nothing to share out; and `whole` or
-// more times as many as the slots.
+// Whole are: segments of few keys, where partial results would cost more than a longer
+// loop (120 segments of 128 rows over 969 keys, head size 128: 24 us whole, 44 dealt; 8
+// tokens over 1000 keys 13.9 / 20.6); and `whole` or more times as many as the slots.
 constexpr int kFewKeys = 1024, kWholeKeys = 16, kWholeRows = 1;
-Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int slots, int whole) {
+Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int slots, int whole, int few) {
   Split pl{};
   pl.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
   pl.unit_shift = unit_shift;
   long long keys = (long long)C.max_pages * C.page;
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
   const long long segments = (long long)C.B * pl.row_tiles * C.Hkv;
-  const bool direct = segments <= (1 << 22) && (keys <= kFewKeys || segments >= (long long)whole * slots);
+  const bool direct = segments <= (1 << 22) && (keys <= few || segments >= (long long)whole * slots);
   pl.workers = direct ? 0 : slots;
   return pl;
 }
@@ -48,7 +49,9 @@ hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, const Split& pl,
 
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys);
+  // wide fp32 products make the loop longer: 8 tokens over 1000 keys, head size 256, 46 us whole, 24 dealt
+  constexpr int kFew = CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys;
+  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys, kFew);
   return run_plan<CT, D, NB * 16>(
       C, a, pl, read_once(C, pl) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
@@ -56,26 +59,33 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 template <int CT, int D>
 hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   using S = RowsShape<CT, D>;
-  const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows);
+  const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows, kFewKeys);
   return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 
 // Workgroups of k_attend_keys that a CU holds, by their registers.
 template <int CT, int D, int NB>
 constexpr int keys_per_cu() {
-  constexpr int kWidth = D / 64 * NB * (CT == DSPARK_F32 ? 2 : 1);
-  return kWidth <= 1 ? 4 : kWidth <= 2 ? 3 : kWidth <= 4 ? 2 : 1;
+  if (CT == DSPARK_F32) return D == 64 ? 5 - NB : D == 128 ? 2 : 1;
+  return D == 64 ? 4 : D == 128 ? 3 : 2;
 }
 
 template <int CT, int D>
 hipError_t run(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   const int rows = max_rows(C, a.c.max_new);
   if (rows <= 16) return run_keys<CT, D, 1, keys_per_cu<CT, D, 1>()>(C, a, s);
-  // fp32 products take 16 times as long as bf16 ones: no kernel that shares loads is needed
-  if constexpr (CT == DSPARK_F32)
-    return run_keys<CT, D, 256 / D, keys_per_cu<CT, D, 256 / D>()>(C, a, s);
-  else
+  if constexpr (CT == DSPARK_F32) {
+    // fp32 products take 8 to 16 times as long as bf16 ones: no kernel that shares loads
+    // through LDS is needed.  32 rows a workgroup read the keys half as often as 16, with
+    // fewer workgroups a CU; head size 128: where they fill the chip (1024 rows x 4 heads
+    // over 4096 keys 294 us against 343), not for fewer (482 rows over 1302 keys 70 against
+    // 64); head size 256: no room.
+    constexpr int kNB = D == 256 ? 1 : 2, kOcc = keys_per_cu<CT, D, kNB>();
+    if (D == 64 || (long long)C.B * C.Hkv * ((rows + 31) / 32) >= kOcc * kCUs) return run_keys<CT, D, kNB, kOcc>(C, a, s);
+    return run_keys<CT, D, 1, keys_per_cu<CT, D, 1>()>(C, a, s);
+  } else {
     return run_rows<CT, D>(C, a, s);
+  }
 }
 
 template <int CT>
@@ -86,9 +96,10 @@ hipError_t run_type(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new) {
-  // the records and two partial results a worker: at most 4 workers a CU with tiles of 16 rows, 2 with 128
-  const bool few = max_rows(C, max_new) <= 16;
-  const int workers = (few ? 4 : 2) * kCUs, rows = few ? 16 : C.cache_dtype == DSPARK_F32 ? 64 : 128;
+  // the records and two partial results a worker: at most 4 workers a CU with tiles of 16
+  // rows (fp32: of 32), 2 with 128
+  const bool few = max_rows(C, max_new) <= 16, f32 = C.cache_dtype == DSPARK_F32;
+  const int workers = (few || f32 ? 4 : 2) * kCUs, rows = few ? 16 : f32 ? 32 : 128;
   return records_bytes(workers) + (size_t)2 * workers * rows * (C.D + 2) * sizeof(float);
 }
 
