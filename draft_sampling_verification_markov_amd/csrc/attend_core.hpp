@@ -46,6 +46,7 @@ struct Split {
   int row_tiles;  // of a request, at most
   int workers;
   int unit_shift;
+  int spread_shift, xcd_tiles;  // of whole segments: XCDs (log2) that share a pair's row tiles, and each one's number
 };
 
 // A partial segment: O (unnormalised) [rows][D], then (m, l) [rows]; two a worker.
@@ -205,23 +206,30 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   return s;
 }
 
-// The segment of a workgroup that takes a whole one.  Workgroups go round the 8 XCDs;
-// a (request, head) pair's row tiles go to one XCD, next to each other, so that they
-// read the keys through one L2 at about the same time; the last ones, which see the
-// most keys, go first.
+// The segment of a workgroup that takes a whole one (none: b = B or row_tile < 0).
+// Workgroups go round the 8 XCDs; a (request, head) pair's row tiles go to one XCD, next to
+// each other, so that they read the keys through one L2 at about the same time; the last
+// ones, which see the most keys, go first.  Pairs that would not fill the XCDs evenly are
+// spread over 2, 4 or 8 of them (2 pairs of 2000 rows x 8 heads, fp32, on 2 XCDs: 630 us).
 __device__ __forceinline__ Start whole_segment(const AttendArgs& a, const Split& p) {
   Start s{};
   const unsigned slot = blockIdx.x >> 3;
-  const unsigned pair = (slot / p.row_tiles << 3) + (blockIdx.x & 7);
-  s.row_tile = p.row_tiles - 1 - (int)(slot % p.row_tiles);
+  const unsigned share = (slot / p.xcd_tiles << 3) + (blockIdx.x & 7), pair = share >> p.spread_shift;
+  const int turn = (int)((slot % p.xcd_tiles << p.spread_shift) + (share & ((1u << p.spread_shift) - 1)));
+  s.row_tile = p.row_tiles - 1 - turn;
   s.head = (int)(pair % a.c.Hkv);
   s.b = (int)(pair / a.c.Hkv);
   s.count = 0x7fffffffffffffffLL;
   return s;
 }
-// workgroups of such a launch: the pairs rounded up to whole rounds of the XCDs
-inline int whole_grid(const dspark_cache& C, const Split& p) {
-  return ((C.B * C.Hkv + 7) & ~7) * p.row_tiles;
+// workgroups of such a launch: the pairs' shares rounded up to whole rounds of the XCDs
+inline int whole_grid(const dspark_cache& C, Split& p) {
+  const int pairs = C.B * C.Hkv;
+  p.spread_shift = 0;
+  // a pair more or less on an XCD is an eighth of its work or less from 64 pairs on
+  while (pairs < 64 && ((pairs << p.spread_shift) & 7) && (2 << p.spread_shift) <= p.row_tiles) ++p.spread_shift;
+  p.xcd_tiles = (p.row_tiles + (1 << p.spread_shift) - 1) >> p.spread_shift;
+  return (((pairs << p.spread_shift) + 7) & ~7) * p.xcd_tiles;
 }
 
 // The next segment that has units (there is one).
@@ -435,19 +443,22 @@ __device__ __forceinline__ void put_record(const Partials& ws, const Start& s, i
   ws.records[worker] = r;
 }
 
-// Joins the partial results of the segment that worker blockIdx.x's first unit lies
-// in, if the worker is the segment's second one.  A row's parts (m, l, O) add up as
+// Joins the partial results of the segment that a worker's first unit lies in, if the
+// worker is the segment's second one.  Equal segments have equally many workers, often a
+// multiple of the 8 XCDs: a segment's workgroups (blockIdx.y) take turns with the XCDs (16
+// segments of 32 parts and 128 rows, all on one XCD: 71 us).  A row's parts (m, l, O) add up as
 // sum exp2(m - M) (l, O), M the largest m, in a fixed order.  Groups of D / 4 threads
 // take a row each; where there are many parts and few rows (tokens over a long context
 // dealt to many workers) the workgroup takes a row, its groups the parts in turn.
 constexpr int join_groups(int rows) { return rows > 64 ? 16 : 8; }  // workgroups of a segment
-constexpr int kFewParts = 8, kMaxParts = 4 * kCUs;  // (the most workers)
+constexpr int kFewParts = 8, kMaxParts = 2 * kCUs;  // (the most workers)
 template <int CT, int D, int ROWS>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Split p) {
   constexpr int kLanes = D / 4, kGroups = kAttendThreads / kLanes;  // a float4 a lane
   const Partials ws = partials(a, p);
-  const Record rec = ws.records[blockIdx.x];
-  if (rec.b < 0 || (int)blockIdx.x != rec.first + 1) return;
+  const int worker = (blockIdx.x + blockIdx.y) % gridDim.x;
+  const Record rec = ws.records[worker];
+  if (rec.b < 0 || worker != rec.first + 1) return;
   const int parts = rec.last - rec.first + 1;
   const Geometry g = geometry<ROWS>(a, p, rec.b, rec.row_tile);
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;

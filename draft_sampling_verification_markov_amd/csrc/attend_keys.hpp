@@ -99,7 +99,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     }
   } else {
     s = whole_segment(a, p);
-    if (s.b >= c.B) return;
+    if (s.b >= c.B || s.row_tile < 0) return;
   }
   long long left = s.count;
   bool first_segment = true;

@@ -106,7 +106,6 @@ struct RowsShape {
   static constexpr int kBytes = kKeys * D * kEs;             // of the keys (or the values) of a tile
   static constexpr int kPieces = D * kEs / 16;               // of a key
   static constexpr int kOps = kBytes / 1024 / 4;               // DMA instructions a wave, keys (or values)
-  static constexpr int kPerCu = 2;                           // workgroups that a CU holds
   static constexpr int kAhead = D == 256 ? 3 : 4;            // LDS reads before their products (more spill at 256)
   static constexpr int kQ = D / 16;                          // registers of Q (16 bytes a lane)
   static constexpr int kBlocks = D / 32;                     // of 32 coordinates
@@ -155,7 +154,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     }
   } else {
     s = whole_segment(a, p);
-    if (s.b >= c.B) return;
+    if (s.b >= c.B || s.row_tile < 0) return;
   }
   long long left = s.count;
   bool first_segment = true;

@@ -9,22 +9,34 @@ namespace {
 
 int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / C.Hkv); }
 
-// Whole segments or dealt units, for a kernel of which the chip holds `slots` workgroups.
-// Whole segments need no partial results, and the row tiles of a head run side by side
-// through one L2; but they leave the chip idle where they are few or of unequal length.
-// Whole are: segments of few keys, where partial results would cost more than a longer
-// loop (120 segments of 128 rows over 969 keys, head size 128: 24 us whole, 44 dealt; 8
-// tokens over 1000 keys 13.9 / 20.6); and `whole` or more times as many as the slots.
-constexpr int kFewKeys = 1024, kWholeKeys = 16, kWholeRows = 1;
-Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int slots, int whole, int few) {
+// Whole segments or dealt units.  Whole segments need no partial results, and the row
+// tiles of a head run side by side through one L2; but they leave the chip idle where they
+// are few or of unequal length.  Whole are:
+//   segments of few keys, where partial results would cost more than a longer loop (120
+//     segments of 128 rows over 969 keys, head size 128: 24 us whole, 44 dealt; 8 tokens
+//     over 1000 keys 13.9 / 20.6);
+//   `whole` segments or more;
+//   with several row tiles a head, whose lengths differ little, one a CU and not many keys
+//     (376 segments of 128 rows over 4096 keys 96 / 105, over 1500 43 / 75; 352 over 16000
+//     354 / 320).
+// Dealt ones go to one worker a CU, or to two where there are enough keys (`twice`): the
+// second hides the other's waits, but doubles the partial results and halves their shares.
+constexpr int kFewKeys = 1024, kSomeKeys = 4096;
+struct Rule {
+  int few;           // keys of a segment
+  long long whole;   // segments
+  long long twice;   // keys of all segments
+};
+Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int per_cu, const Rule& r) {
   Split pl{};
   pl.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
   pl.unit_shift = unit_shift;
   long long keys = (long long)C.max_pages * C.page;
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
   const long long segments = (long long)C.B * pl.row_tiles * C.Hkv;
-  const bool direct = segments <= (1 << 22) && (keys <= few || segments >= (long long)whole * slots);
-  pl.workers = direct ? 0 : slots;
+  const bool direct = segments <= (1 << 22) && (keys <= r.few || segments >= r.whole ||
+                                                (pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
+  pl.workers = direct ? 0 : per_cu > 1 && segments * keys >= r.twice ? 2 * kCUs : kCUs;
   return pl;
 }
 
@@ -37,9 +49,10 @@ bool read_once(const dspark_cache& C, const Split& pl) {
 }
 
 template <int CT, int D, int ROWS, typename Kernel>
-hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, const Split& pl, Kernel kernel, hipStream_t s) {
+hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, Split pl, Kernel kernel, hipStream_t s) {
   if (!pl.workers) {
-    kernel<<<whole_grid(C, pl), kAttendThreads, 0, s>>>(a, pl);
+    const int grid = whole_grid(C, pl);
+    kernel<<<grid, kAttendThreads, 0, s>>>(a, pl);
     return hipGetLastError();
   }
   kernel<<<pl.workers, kAttendThreads, 0, s>>>(a, pl);
@@ -49,9 +62,13 @@ hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, const Split& pl,
 
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  // wide fp32 products make the loop longer: 8 tokens over 1000 keys, head size 256, 46 us whole, 24 dealt
-  constexpr int kFew = CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys;
-  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC * kCUs, kWholeKeys, kFew);
+  // `few`: wide fp32 products make the loop longer: 8 tokens over 1000 keys, head size 256,
+  // 46 us whole, 24 dealt.  `twice`: for a few rows (memory bound) one worker a CU suffices
+  // for long: a token over 20000 keys 15.9 us with one, 18.8 with two, 3 requests over
+  // 150000 keys x 4 heads 108 / 111, 200 over 3000 x 8 heads 250 / 244; for more rows, 608
+  // segments of 3000 keys, 133 / 111.
+  constexpr Rule kRule{CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys, 16 * OCC * kCUs, NB == 1 ? 1 << 22 : 1 << 20};
+  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC, kRule);
   return run_plan<CT, D, NB * 16>(
       C, a, pl, read_once(C, pl) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
@@ -59,7 +76,10 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 template <int CT, int D>
 hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   using S = RowsShape<CT, D>;
-  const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, S::kPerCu * kCUs, kWholeRows, kFewKeys);
+  // `twice`: 12 segments of 17123 keys 42 us with one worker a CU, 50 with two; 20 of 132768
+  // 159 / 115
+  constexpr Rule kRule{kFewKeys, 2 * kCUs, 1 << 20};
+  const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, 2, kRule);
   return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 
@@ -96,10 +116,8 @@ hipError_t run_type(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new) {
-  // the records and two partial results a worker: at most 4 workers a CU with tiles of 16
-  // rows (fp32: of 32), 2 with 128
-  const bool few = max_rows(C, max_new) <= 16, f32 = C.cache_dtype == DSPARK_F32;
-  const int workers = (few || f32 ? 4 : 2) * kCUs, rows = few ? 16 : f32 ? 32 : 128;
+  // the records and two partial results a worker
+  const int workers = 2 * kCUs, rows = max_rows(C, max_new) <= 16 ? 16 : C.cache_dtype == DSPARK_F32 ? 32 : 128;
   return records_bytes(workers) + (size_t)2 * workers * rows * (C.D + 2) * sizeof(float);
 }
 

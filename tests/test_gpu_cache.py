@@ -117,6 +117,15 @@ def test_attend_row_counts(ds, dtype, D, page, rows, G, wide):
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f8", 128), ("f32", 64), ("f32", 256)])
+@pytest.mark.parametrize("n_new,length,Hkv", [([600], [700], 1), ([257, 0, 90, 300, 129], [257, 8, 95, 310, 129], 1),
+                                              ([150, 33], [200, 700], 3)])
+def test_attend_row_tiles_of_few_heads(ds, dtype, D, n_new, length, Hkv):
+    # many row tiles of fewer (request, head) pairs than the chip's parts, and of numbers that these do not divide
+    c = cu.make(33, dtype, 32, D, 4 * Hkv, Hkv, n_new, length, gap=1)
+    check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_attend_window_of_any_size(ds, causal):
     # fewer cached tokens than rows, and windows up to the largest integer: the same as none
