@@ -13,8 +13,8 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // tiles of a head run side by side through one L2; but they leave the chip idle where they
 // are few or of unequal length.  Whole are:
 //   segments of few keys, where partial results would cost more than a longer loop (120
-//     segments of 128 rows over 969 keys, head size 128: 24 us whole, 44 dealt; 8 tokens
-//     over 1000 keys 13.9 / 20.6);
+//     segments of 128 rows over 969 keys, head size 128: 24 us whole, 34 dealt; 128
+//     segments of a token over 900 keys 15 / 22);
 //   `whole` segments or more;
 //   with several row tiles a head, whose lengths differ little, one a CU and not many keys
 //     (376 segments of 128 rows over 4096 keys 96 / 105, over 1500 43 / 75; 352 over 16000
@@ -23,9 +23,9 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // second hides the other's waits, but doubles the partial results and halves their shares.
 constexpr int kFewKeys = 1024, kSomeKeys = 4096;
 struct Rule {
-  int few;           // keys of a segment
-  long long whole;   // segments
-  long long twice;   // keys of all segments
+  int few;          // keys of a segment, of fewer than half as many as CUs (kFewKeys for more)
+  long long whole;  // segments
+  long long twice;  // keys of all segments
 };
 Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int per_cu, const Rule& r) {
   Split pl{};
@@ -34,7 +34,7 @@ Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int
   long long keys = (long long)C.max_pages * C.page;
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
   const long long segments = (long long)C.B * pl.row_tiles * C.Hkv;
-  const bool direct = segments <= (1 << 22) && (keys <= r.few || segments >= r.whole ||
+  const bool direct = segments <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
                                                 (pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
   pl.workers = direct ? 0 : per_cu > 1 && segments * keys >= r.twice ? 2 * kCUs : kCUs;
   return pl;
@@ -62,8 +62,8 @@ hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, Split pl, Kernel
 
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
-  // `few`: wide fp32 products make the loop longer: 8 tokens over 1000 keys, head size 256,
-  // 46 us whole, 24 dealt.  `twice`: for a few rows (memory bound) one worker a CU suffices
+  // `few`: wide fp32 products make the loop longer: 32 segments of 1000 keys, head size 256,
+  // 46 us whole, 24 dealt, but 512 segments of 900 keys 121 / 126, head size 128 61 / 72.  `twice`: for a few rows (memory bound) one worker a CU suffices
   // for long: a token over 20000 keys 15.9 us with one, 18.8 with two, 3 requests over
   // 150000 keys x 4 heads 108 / 111, 200 over 3000 x 8 heads 250 / 244; for more rows, 608
   // segments of 3000 keys, 133 / 111.
