@@ -104,6 +104,8 @@ hipError_t run(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
     if (D == 64 || (long long)C.B * C.Hkv * ((rows + 31) / 32) >= kOcc * kCUs) return run_keys<CT, D, kNB, kOcc>(C, a, s);
     return run_keys<CT, D, 1, keys_per_cu<CT, D, 1>()>(C, a, s);
   } else {
+    // (k_attend_keys with 32 rows: 256 requests of 28 rows over 2000 keys 226 us against 172,
+    // 8 of 32 rows 29 against 24; only at 20 rows it gains a little, 40 against 42)
     return run_rows<CT, D>(C, a, s);
   }
 }
