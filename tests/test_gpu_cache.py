@@ -126,6 +126,25 @@ def test_attend_row_tiles_of_few_heads(ds, dtype, D, n_new, length, Hkv):
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f8", "f32"])
+@pytest.mark.parametrize("rows", [1, 9])
+def test_attend_many_requests_dealt(ds, dtype, rows):
+    # more requests than a workgroup has threads, ragged, some without new tokens or without any, in a wide page table
+    i = np.arange(620)
+    length = np.where(i % 7 == 3, 0, 1 + (i * 37) % 90)
+    length[[0, 255, 256, 511, 619]] = 2100, 70, 1, 0, 1300
+    n_new = np.where(i % 5 == 4, 0, np.minimum(1 + i % rows, np.maximum(length, 1)))
+    c = cu.make(34, dtype, 32, 64, 4, 1, n_new, length, width=100, poison=False)
+    check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
+
+
+@pytest.mark.parametrize("dtype,D,n", [("f32", 256, 530), ("bf16", 64, 4200)])
+def test_attend_many_row_tiles_dealt(ds, dtype, D, n):
+    # more row tiles of a request than a workgroup has threads; the page table's width has the keys dealt
+    c = cu.make(35, dtype, 64, D, 8, 1, [n], [n + 70], width=6000 // 64, poison=False)
+    check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_attend_window_of_any_size(ds, causal):
     # fewer cached tokens than rows, and windows up to the largest integer: the same as none
