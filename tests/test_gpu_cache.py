@@ -420,7 +420,7 @@ def test_update_and_compact_of_random_sequences(ds, cache, page, layers, Hkv, D)
     p.compact()
 
 
-@pytest.mark.parametrize("n_pages", [1, 4095, 4096, 4097, 9000])
+@pytest.mark.parametrize("n_pages", [1, 4095, 4096, 4097, 9000, 9216, 32768, 32769])
 def test_pages_around_the_scan_blocks(ds, n_pages):
     B = 5
     p = Pages(ds, B, n_pages, 16, max(1, n_pages // 3), seed=1)
@@ -432,8 +432,8 @@ def test_pages_around_the_scan_blocks(ds, n_pages):
     p.update(np.array([1, 16, 1, 5, 1]))
 
 
-def test_update_many_slots(ds):
-    B = 700
+@pytest.mark.parametrize("B", [700, 1024, 1100])
+def test_update_many_slots(ds, B):
     p = Pages(ds, B, 3000, 16, 9, seed=2)
     rng = np.random.default_rng(4)
     p.update(rng.integers(0, 100, B))
