@@ -89,7 +89,9 @@ size_t dspark_cache_workspace_bytes(const dspark_cache* C, int32_t max_new);
  * In/out:  k_pool, v_pool: layer `layer` receives the tokens; nothing else changes.
  * An e4m3 cache stores x / scale rounded to nearest (ties to even), values past
  * +-448 as +-448, NaN as NaN.  A page that several slots hold must not be written
- * (dspark_cache_update gives every growing slot a private one).  n_rows = 0 does
+ * (dspark_cache_update gives every growing slot a private one).  Of 8 neighbouring
+ * tokens that are not all new the others' values are read and written back as they
+ * are: two calls that append to one page have to be ordered.  n_rows = 0 does
  * nothing.
  */
 dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const void* k, int64_t k_stride, const void* v,
