@@ -47,6 +47,7 @@ struct Split {
   int workers;
   int unit_shift;
   int spread_shift, xcd_tiles;  // of whole segments: XCDs (log2) that share a pair's row tiles, and each one's number
+  bool longest_first;           // of whole segments: requests in descending order of their length
 };
 
 // A partial segment: O (unnormalised) [rows][D], then (m, l) [rows]; two a worker.
@@ -206,6 +207,27 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   return s;
 }
 
+// The request with the n-th largest length (of equal ones the first), by counting: every
+// thread ranks its own.  Up to kAttendThreads requests.
+__device__ __forceinline__ int nth_longest(const AttendArgs& a, int n) {
+  static_assert(kAttendThreads == 256, "a length (24 bits) and the thread's number share a word");
+  __shared__ __attribute__((aligned(16))) uint32_t key[kAttendThreads];
+  __shared__ int found;
+  const int t = threadIdx.x, B = a.c.B;
+  const int len = t < B && a.c.rows(t) > 0 ? min(a.c.len(t), (1 << 24) - 1) : 0;
+  const uint32_t mine = t < B ? ((uint32_t)len << 8) + (255 - t) : 0;
+  key[t] = mine;
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < B; i += 4) {  // (keys past B are 0: not larger than any)
+    const uint4 k = *reinterpret_cast<const uint4*>(key + i);
+    rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+  }
+  if (t < B && rank == n) found = t;
+  __syncthreads();
+  return found;
+}
+
 // The segment of a workgroup that takes a whole one (none: b = B or row_tile < 0).
 // Workgroups go round the 8 XCDs; a (request, head) pair's row tiles go to one XCD, next to
 // each other, so that they read the keys through one L2 at about the same time; the last
@@ -220,6 +242,7 @@ __device__ __forceinline__ Start whole_segment(const AttendArgs& a, const Split&
   s.head = (int)(pair % a.c.Hkv);
   s.b = (int)(pair / a.c.Hkv);
   s.count = 0x7fffffffffffffffLL;
+  if (p.longest_first && s.b < a.c.B && s.row_tile >= 0) s.b = nth_longest(a, s.b);
   return s;
 }
 // workgroups of such a launch: the pairs' shares rounded up to whole rounds of the XCDs

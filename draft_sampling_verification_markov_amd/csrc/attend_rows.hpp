@@ -8,7 +8,7 @@
 // 128, bf16 (590 GFLOP) 557 us, 1.06 PFLOP/s, the matrix units busy in 52% of the cycles
 // (8 waves, half of them in their products and half in the softmax by barriers, 706; 64
 // rows a wave 1272, for the moves between its registers); 256 x up to 17 tokens over up to
-// 2048 keys (0.98 GB) 190 us, 5.2 TB/s.
+// 2048 keys (0.98 GB) 183 us, 5.4 TB/s.
 //
 // A tile of kKeys keys and values comes by LDS DMA (16 bytes a lane) into one of two
 // buffers while the other is used; the buffers are distinct __shared__ objects, so that

@@ -138,6 +138,20 @@ def test_attend_many_requests_dealt(ds, dtype, rows):
     check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f8", "f32"])
+@pytest.mark.parametrize("B,Hkv", [(70, 8), (256, 3), (257, 2)])
+def test_attend_many_ragged_segments(ds, dtype, B, Hkv):
+    # more segments than run at once, of unequal and of equal lengths, over more keys than a few
+    i = np.arange(B)
+    length = 30 + (i * 53) % 200
+    length[[1, 5, B - 1]] = 1100, 1100, 900
+    length[[0, 7]] = 0, 0
+    n_new = np.where(i % 4 == 2, 0, np.minimum(2 + (i * 5) % 8, length))
+    n_new[1] = 40
+    c = cu.make(36, dtype, 32, 64, 2 * Hkv, Hkv, n_new, length, width=40, poison=False)
+    check_attend(c, *gpu_attend(ds, c), cu.oracle_attend(c))
+
+
 @pytest.mark.parametrize("dtype,D,n", [("f32", 256, 530), ("bf16", 64, 4200)])
 def test_attend_many_row_tiles_dealt(ds, dtype, D, n):
     # more row tiles of a request than a workgroup has threads; the page table's width has the keys dealt
