@@ -72,8 +72,13 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   // for long: a token over 20000 keys 15.9 us with one, 18.8 with two, 3 requests over
   // 150000 keys x 4 heads 108 / 111, 200 over 3000 x 8 heads 250 / 244; for more rows, 608
   // segments of 3000 keys, 133 / 111.
-  constexpr Rule kRule{CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys, 16 * OCC * kCUs, NB == 1 ? 1 << 22 : 1 << 20};
-  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC, kRule);
+  // `whole`: as many as the chip holds, where the longest go first (256 tokens over up to
+  // 4096 keys x 8 heads 375 us whole, 402 dealt; 256 over 2000 x 4, e4m3, 58 / 84); many more
+  // where they cannot be ordered.
+  constexpr int kHeld = (OCC > 2 ? OCC : 2) * kCUs;
+  const Rule rule{CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys, C.B <= kAttendThreads ? kHeld : 16 * kHeld,
+                  NB == 1 ? 1 << 22 : 1 << 20};
+  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC, rule);
   return run_plan<CT, D, NB * 16>(
       C, a, pl, read_once(C, pl) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
