@@ -46,9 +46,9 @@ Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int
 }
 
 // Keys that one workgroup reads, and that the 256 MB last-level cache does not hold until
-// the next call, are read with the streaming policy: 256 requests x 17 rows 205 -> 192 us,
-// 256 x 1 421 -> 402.  For others it costs: prompts, whose row tiles meet in L2, 567 -> 603,
-// 72 MB of keys 28 -> 33.
+// the next call, are read with the streaming policy: 256 requests x 17 rows 191 -> 182 us,
+// 256 x 1 402 -> 374.  For others it costs: prompts, whose row tiles meet in L2, 563 -> 589,
+// 64 tokens over 2000 keys x 2 heads (72 MB) 27.8 -> 29.6.
 bool read_once(const dspark_cache& C, const Split& pl) {
   return pl.row_tiles == 1 && 2 * page_bytes(C) * C.n_pages > ((size_t)256 << 20);
 }
