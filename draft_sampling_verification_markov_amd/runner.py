@@ -124,6 +124,7 @@ class PagedCache:
                        torch.zeros(C.B, dtype=i32, device=device), torch.zeros(C.n_pages, dtype=i32, device=device))
                       for _ in range(2)]
         self.n_short = torch.zeros(1, dtype=i32, device=device)
+        self._none_short = torch.zeros_like(self.n_short)
         self.n_live = torch.zeros(1, dtype=i32, device=device)
         nbytes = dspark.cache_workspace_bytes(C, self.max_new)
         if nbytes == 0:
@@ -134,10 +135,12 @@ class PagedCache:
     length = property(lambda self: self._sets[0][1])
     ref = property(lambda self: self._sets[0][2])
 
-    def update(self, new_len, parent=None, stream=None):
-        """Every slot's next sequence (dspark_cache_update); n_short tells the pages that were missing."""
+    def update(self, new_len, parent=None, stream=None, n_short=None):
+        """Every slot's next sequence (dspark_cache_update); n_short (the cache's own, unless another is given) tells
+        the pages that were missing."""
         now, new = self._sets
-        dspark.cache_update(self.C, parent, new_len, *now, *new, self.n_short, self.k, self.v, self.workspace, stream)
+        dspark.cache_update(self.C, parent, new_len, *now, *new, self.n_short if n_short is None else n_short, self.k,
+                            self.v, self.workspace, stream)
         self._sets.reverse()
 
     def compact(self, stream=None):
@@ -162,8 +165,11 @@ def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forw
     After the schedule the cache grows by the n_sched + 1 rows of every request (the anchor and its
     drafts); forward(tokens [B][K + 1], n_new [B]) runs the target over them (cache.append and
     cache.attend per layer, rows b * (K + 1) ..) and leaves its logits in x.Zt; after the verification
-    the cache keeps the anchor and the accepted drafts.  Where the pool cannot hold a request's rows,
-    cache.n_short is positive, n_new[b] is 0 and what the cycle emits for that request is unspecified."""
+    the cache keeps the anchor and the accepted drafts.
+
+    Returns n_new [B], the rows that each request got.  Where the pool cannot hold a request's rows it gets none
+    (n_new 0), and cache.n_short tells the pages that were missing.  A request without rows emits nothing: its out_tok
+    is -1 throughout, n_acc -1, its next_anchor its anchor, and its sequence stays as it was."""
     draft(P, x, o, path=path)
     schedule(P, x, o)
     before = cache.length
@@ -171,4 +177,12 @@ def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forw
     n_new = cache.length - before
     forward(torch.cat([x.anchor[:, None], o.tok], 1), n_new)
     verify(P, x, o)
-    cache.update(torch.minimum(before + o.n_acc + 1, cache.length))
+    # what verify made of logits that no forward pass wrote
+    none = n_new == 0
+    o.n_acc.masked_fill_(none, -1)
+    o.out_tok.masked_fill_(none[:, None], -1)
+    o.logp.masked_fill_(none[:, None], float("nan"))
+    o.resid_mass.masked_fill_(none, float("nan"))
+    o.next_anchor.copy_(torch.where(none, x.anchor, o.next_anchor))
+    cache.update(torch.minimum(before + o.n_acc + 1, cache.length), n_short=cache._none_short)  # (this one only shrinks)
+    return n_new
