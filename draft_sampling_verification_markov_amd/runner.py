@@ -92,8 +92,9 @@ def schedule(P, x: CycleInputs, o: CycleOutputs, stream=None):
     dspark.schedule(P, o.surv, x.T, o.n_sched, o.n_total, o.workspace, stream)
 
 
-def verify(P, x: CycleInputs, o: CycleOutputs, stream=None):
-    dspark.verify(P, x.Zt, x.Z, x.E, x.Wt, x.anchor, o.tok, o.logq, o.lse, o.n_sched,
+def verify(P, x: CycleInputs, o: CycleOutputs, stream=None, n_sched=None):
+    """n_sched: the drafts to judge, the schedule's unless others are given."""
+    dspark.verify(P, x.Zt, x.Z, x.E, x.Wt, x.anchor, o.tok, o.logq, o.lse, o.n_sched if n_sched is None else n_sched,
                   o.out_tok, o.n_acc, o.next_anchor, o.logp, o.resid_mass, o.workspace, stream)
 
 
@@ -168,15 +169,17 @@ def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forw
     the cache keeps the anchor and the accepted drafts.
 
     Returns n_new [B], the rows that each request got.  Where the pool cannot hold a request's rows it gets none
-    (n_new 0), and cache.n_short tells the pages that were missing.  A request without rows emits nothing: its out_tok
-    is -1 throughout, n_acc -1, its next_anchor its anchor, and its sequence stays as it was."""
+    (n_new 0), and cache.n_short tells the pages that were missing; at the end of its row of the page table it gets those
+    that fit.  Of n_new rows the first n_new - 1 drafts are judged (o.n_sched stays the schedule's).  A request without
+    rows emits nothing: its out_tok is -1 throughout, n_acc -1, its next_anchor its anchor, and its sequence stays as
+    it was."""
     draft(P, x, o, path=path)
     schedule(P, x, o)
     before = cache.length
     cache.update(before + o.n_sched + 1)
     n_new = cache.length - before
     forward(torch.cat([x.anchor[:, None], o.tok], 1), n_new)
-    verify(P, x, o)
+    verify(P, x, o, n_sched=(n_new - 1).clamp(min=0))
     # what verify made of logits that no forward pass wrote
     none = n_new == 0
     o.n_acc.masked_fill_(none, -1)
@@ -184,5 +187,5 @@ def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forw
     o.logp.masked_fill_(none[:, None], float("nan"))
     o.resid_mass.masked_fill_(none, float("nan"))
     o.next_anchor.copy_(torch.where(none, x.anchor, o.next_anchor))
-    cache.update(torch.minimum(before + o.n_acc + 1, cache.length), n_short=cache._none_short)  # (this one only shrinks)
+    cache.update(before + o.n_acc + 1, n_short=cache._none_short)  # (this one only shrinks)
     return n_new

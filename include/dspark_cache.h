@@ -16,6 +16,10 @@
  *   per layer: dspark_cache_append, dspark_cache_attend,
  *   dspark_verify,
  *   dspark_cache_update (the accepted length).
+ * A request gets n_new = length_out - length rows from the first update: fewer than
+ * n_sched + 1 at the end of its row of the page table, none where the pool has no room.
+ * Those are the counts for append and attend, and dspark_verify may judge n_new - 1
+ * drafts at most: the target has no logits for more.
  *
  * The cache.  Request slot b holds length[b] tokens in the pages
  * table[b][0 .. ceil(length[b] / page) - 1]; token j lies in page table[b][j / page]

@@ -104,3 +104,12 @@ def test_a_pool_without_room_is_reported(world):
     got = world[1].run_cached_cycle(P, x, o, cache, forward)
     check(x, o, cache, [0, 16, 0, 16], [4, 4, 0, 0], got)
     assert int(cache.n_short) == 2
+
+
+def test_the_end_of_the_table_row(world):
+    # rows of two pages: slot 0 has room for 2 of its 4 tokens, slot 1 for none, slot 2 for 1 of 3, slot 3 for its one
+    lengths = [30, 32, 31, 31]
+    P, x, o, cache, forward = start(*world, 40, 2, lengths)
+    got = world[1].run_cached_cycle(P, x, o, cache, forward)
+    check(x, o, cache, lengths, [2, 0, 1, 1], got)
+    assert (cache.length <= 32).all() and int(cache.n_short) == 0

@@ -79,3 +79,13 @@ def test_a_pool_without_room(lib, stale):
     x, o, n_new, cache, plain = cycle(lib, 5, 4, lengths, stale)
     assert n_new == [5, 0, 5, 0, 5] and int(cache.n_short.item()) == 2
     check(x, o, n_new, cache, plain, lengths)
+
+
+@pytest.mark.parametrize("stale", [0.0, 1e4])
+def test_the_end_of_the_table_row(lib, stale):
+    # rows of 32 tokens: room for 2 of 5 rows, for none, for one, for four, for all
+    lengths = [30, 32, 31, 28, 3]
+    x, o, n_new, cache, plain = cycle(lib, 20, 2, lengths, stale)
+    assert n_new == [2, 0, 1, 4, 5] and int(cache.n_short.item()) == 0
+    check(x, o, n_new, cache, plain, lengths)
+    assert (cache.length <= 32).all()
