@@ -172,7 +172,13 @@ def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forw
     (n_new 0), and cache.n_short tells the pages that were missing; at the end of its row of the page table it gets those
     that fit.  Of n_new rows the first n_new - 1 drafts are judged (o.n_sched stays the schedule's).  A request without
     rows emits nothing: its out_tok is -1 throughout, n_acc -1, its next_anchor its anchor, and its sequence stays as
-    it was."""
+    it was.
+
+    The cache's slots are the problem's requests, and its max_new is K + 1; with a larger one (ValueError for a smaller)
+    forward has to pass row_start, since without it request b's rows begin at b * max_new."""
+    if cache.C.B != P.B or cache.max_new < P.K + 1:
+        raise ValueError(f"a cache of {cache.C.B} slots and up to {cache.max_new} new rows a slot for {P.B} requests of "
+                         f"up to {P.K + 1}")
     draft(P, x, o, path=path)
     schedule(P, x, o)
     before = cache.length

@@ -113,3 +113,12 @@ def test_the_end_of_the_table_row(world):
     got = world[1].run_cached_cycle(P, x, o, cache, forward)
     check(x, o, cache, lengths, [2, 0, 1, 1], got)
     assert (cache.length <= 32).all() and int(cache.n_short) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(max_new=K), dict(slots=B + 1), dict(slots=B - 1)], ids=str)
+def test_a_cache_of_another_shape_is_refused(world, kw):
+    # fewer rows a call than a cycle can schedule, or other slots than the problem's requests
+    P, x, o, cache, forward = start(*world, 40, 2, None, **kw)
+    with pytest.raises(ValueError):
+        world[1].run_cached_cycle(P, x, o, cache, forward)
+    assert cache.length.tolist() == [0] * cache.C.B
