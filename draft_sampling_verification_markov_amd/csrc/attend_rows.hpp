@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
           else if (r >= 0)
             store4<CT>(a.out, r * a.out_stride + (size_t)hq * D + d, y);
         }
-      if (any_odd) {
+      if (any_odd && !none) {
         const int pos = g.pos0 + (g.row0 + rho) / G;
 #pragma unroll 1
         for (int d = 4 * h; d < D; d += 8) {
