@@ -20,8 +20,9 @@
 // Scores are replaced before the exponential.  In the tiles that some rows see in part
 // or not at all (the sequence's end, the diagonal, a window's edge) values that are not
 // finite are replaced by 0; if a row does see one, the coordinate's result is made NaN
-// or infinite when it is stored (add_nonfinite), from the values themselves.  All other
-// tiles are seen whole by all rows and need no such care.
+// or infinite when it is stored (add_nonfinite), from the values themselves, by a walk over
+// the keys of these tiles.  One that no row sees (behind the sequence's end) costs no walk.
+// All other tiles are seen whole by all rows and need no such care.
 #pragma once
 
 #include <type_traits>
@@ -362,6 +363,32 @@ __device__ __forceinline__ V finite_part(V x) {
   __builtin_memcpy(&x, w, sizeof(V));
   return x;
 }
+// All bits of the elements of a V whose keys lie in [lo, hi).  V: neighbouring tokens of a
+// coordinate from key `first` on, at most 8 (then those of the next coordinate).
+template <int CT, typename V>
+struct KeysWithin {
+  uint32_t mask[sizeof(V) / 4];
+  __device__ __forceinline__ KeysWithin(int first, int lo, int hi) {
+    constexpr int kOf = 4 / Operand<CT>::kBytes, kBits = 32 / kOf;  // elements of a word
+    const int keys = (int)((1u << min(max(hi - first, 0), 8)) - (1u << min(max(lo - first, 0), 8)));  // (lo <= hi)
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(V) / 4); ++i) {
+      mask[i] = 0;
+#pragma unroll
+      for (int e = 0; e < kOf; ++e)
+        mask[i] |= (uint32_t)(keys << (31 - ((i * kOf + e) & 7)) >> 31) & (0xFFFFFFFFu >> (32 - kBits) << (kBits * e));
+    }
+  }
+  // x without the elements of other keys
+  __device__ __forceinline__ V of(V x) const {
+    uint32_t w[sizeof(V) / 4];
+    __builtin_memcpy(w, &x, sizeof(V));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(V) / 4); ++i) w[i] &= mask[i];
+    __builtin_memcpy(&x, w, sizeof(V));
+    return x;
+  }
+};
 
 template <int CT, typename V>
 __device__ __forceinline__ bf16x8_t value_operand(const V& v) {
@@ -401,25 +428,38 @@ __device__ __forceinline__ float cached(const char* p) {
 
 // What the values that are not finite make of coordinates d .. d + 3 of the row at
 // position pos: those of the keys in [k0, k1) that it sees, in tiles of TILE keys that
-// are not wholly in [all_lo, all_hi) (the others' products took them as they are).
+// are not wholly in [all_lo, all_hi) (the others' products took them as they are).  A walk
+// over groups of 8 keys, whose values of 4 coordinates lie together.
 template <int CT, int D, int TILE>
 __device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometry& g, const Masks& mask, int head,
                                               int pos, int d, int k0, int k1, float4& y) {
+  constexpr int kEs = Operand<CT>::kBytes;
   const CacheView& c = a.c;
   const int lo = max(k0, mask.lo(pos)), hi = min(k1, mask.hi(pos));
-  for (int key = lo; key < hi; ++key) {
-    const int tile = key & ~(TILE - 1);
-    if (tile >= g.all_lo && tile + TILE <= g.all_hi) continue;
-    const unsigned page = min((unsigned)c.table[(size_t)g.b * c.max_pages + (key >> c.page_shift)], (unsigned)c.n_pages - 1u);
-    const size_t token = (((size_t)page * c.Hkv + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
-    const char* src = static_cast<const char*>(a.v_pool) +
-                      ((token & ~(size_t)7) * D + (size_t)d * 8 + (token & 7)) * Operand<CT>::kBytes;
-    float* const out = &y.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = cached<CT>(src + i * 8 * Operand<CT>::kBytes);
-      if (!(fabsf(x) < INFINITY)) out[i] += x;
+  const int whole0 = (g.all_lo + TILE - 1) & ~(TILE - 1), whole1 = g.all_hi & ~(TILE - 1);  // the others' tiles
+  for (int j0 = lo & ~7; j0 < hi; j0 += 8) {
+    if (j0 >= whole0 && j0 < whole1) {
+      j0 = whole1 - 8;
+      continue;
     }
+    const unsigned page = min((unsigned)c.table[(size_t)g.b * c.max_pages + (j0 >> c.page_shift)], (unsigned)c.n_pages - 1u);
+    const size_t token = (((size_t)page * c.Hkv + head) << c.page_shift) + (j0 & ((1 << c.page_shift) - 1));
+    const char* src = static_cast<const char*>(a.v_pool) + (token * D + (size_t)d * 8) * kEs;
+    uint4 w[2 * kEs];
+#pragma unroll
+    for (int i = 0; i < 2 * kEs; ++i) w[i] = reinterpret_cast<const uint4*>(src)[i];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * kEs; ++i) find_nonfinite<CT>(w[i], bits);
+    if (!(bits & kOdd<CT>)) continue;
+    float* const out = &y.x;
+#pragma unroll 1
+    for (int key = max(j0, lo); key < min(j0 + 8, hi); ++key)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = cached<CT>(src + (8 * i + (key & 7)) * kEs);
+        if (!(fabsf(x) < INFINITY)) out[i] += x;
+      }
   }
 }
 

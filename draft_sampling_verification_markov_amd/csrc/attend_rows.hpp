@@ -142,7 +142,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
   constexpr int kWavesPerSub16 = 4 / (S::kKeys / 16);  // waves that share the DMA of 16 keys
   __shared__ __attribute__((aligned(1024))) unsigned char k0[S::kBytes], k1[S::kBytes], v0[S::kBytes], v1[S::kBytes];
   __shared__ int sh[4];
-  __shared__ int odd;  // a value that is not finite was replaced
+  __shared__ int odd;  // a value that is not finite, and that a row sees, was replaced
   const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const CacheView& c = a.c;
@@ -312,10 +312,15 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
 #pragma unroll
         for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i) find_nonfinite<CT>(mine[i * kAttendThreads], bits);
         if (__any(bits & kOdd<CT>)) {
-          odd = 1;
 #pragma unroll 1
-          for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i)
-            mine[i * kAttendThreads] = finite_part<CT>(mine[i * kAttendThreads]);
+          for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i) {
+            const int group = (threadIdx.x + i * kAttendThreads) * 16 / (8 * D * kEs);  // of 8 keys
+            const uint4 x = mine[i * kAttendThreads];
+            uint32_t seen = 0;
+            find_nonfinite<CT>(KeysWithin<CT, uint4>(key0 + 8 * group, g.lo, g.hi).of(x), seen);
+            if (seen & kOdd<CT>) odd = 1;
+            mine[i * kAttendThreads] = finite_part<CT>(x);
+          }
         }
         barrier_lds_only();
       }
