@@ -405,7 +405,7 @@ def _rows(t, dtype, shape, index, name):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
         _refuse(t, dtype, shape, index, name)
     s = t.stride()
-    if s[2] != 1 or s[1] != shape[2]:
+    if s[2] != 1 or (s[1] != shape[2] and shape[1] != 1):  # (of one head the stride says nothing)
         raise ValueError(f"{name}'s rows must be dense")
     return t.data_ptr(), s[0]
 
