@@ -402,7 +402,7 @@ def _opt(t, dtype, shape, index, name):
 
 def _rows(t, dtype, shape, index, name):
     """(address, row stride) of [rows][heads][D] whose rows are dense but may lie apart."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
         _refuse(t, dtype, shape, index, name)
     s = t.stride()
     if s[2] != 1 or (s[1] != shape[2] and shape[1] != 1):  # (of one head the stride says nothing)
@@ -410,8 +410,19 @@ def _rows(t, dtype, shape, index, name):
     return t.data_ptr(), s[0]
 
 
+def _count(t, name):
+    """The rows of a [rows][heads][D] array."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows][heads][D]")
+    return t.shape[0]
+
+
 def _device(t):
     """The device of the call: that of its tensors, which has to be the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("k_pool must be a torch.Tensor")
     index = t.get_device()
     if index < 0:
         raise ValueError("the cache's tensors must be device tensors")
@@ -421,6 +432,8 @@ def _device(t):
 
 
 def _workspace(t, index):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if t.get_device() != index:
         raise ValueError(f"workspace is on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
@@ -433,7 +446,7 @@ def cache_append(C: Cache, layer: int, k, v, n_new, row_start, max_new: int, len
     """The new tokens' keys and values (rows of k and v [rows][Hkv][D]) into layer `layer` of the pools."""
     lib, dev = load(), _device(k_pool)
     i32, f32, B, dt, ct = torch.int32, torch.float32, (C.B,), C.data_type, C.cache_type
-    rows = k.shape[0]
+    rows = _count(k, "k")
     kp, ks = _rows(k, dt, (rows, C.Hkv, C.D), dev, "k")
     vp, vs = _rows(v, dt, (rows, C.Hkv, C.D), dev, "v")
     st = lib.dspark_cache_append(
@@ -451,7 +464,7 @@ def cache_attend(C: Cache, layer: int, q, n_new, row_start, max_new: int, length
     """Attention of the rows of q [rows][Hq][D] over their requests' pages; scale None is D ** -0.5."""
     lib, dev = load(), _device(k_pool)
     i32, f32, B, dt, ct = torch.int32, torch.float32, (C.B,), C.data_type, C.cache_type
-    rows = q.shape[0]
+    rows = _count(q, "q")
     qp, qs = _rows(q, dt, (rows, C.Hq, C.D), dev, "q")
     op, os_ = _rows(out, dt, (rows, C.Hq, C.D), dev, "out")
     ws, nbytes = _workspace(workspace, dev)
