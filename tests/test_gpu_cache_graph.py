@@ -1,6 +1,7 @@
 """A captured chain of the cache's calls (fork, append, attend, compact), every replay against the
 oracle: the graph's outputs are buffers of its own that hold a mark before each replay, so a call
-that did nothing in it would show."""
+that did nothing in it would show.  And a captured decoding cycle over a cache, replayed from token
+to token up to the end of the cache's rows, against the same cycles outside a graph."""
 from __future__ import annotations
 
 import numpy as np
@@ -112,3 +113,58 @@ def test_fork_append_attend_compact_replayed(ds, n_pages, dtype):  # noqa: F811
                 y[:, b] = x[:, a]
             np.testing.assert_array_equal(got.cpu().double().numpy(), y)
         _ = (kp.float().nan_to_num().abs().amax() + out.float().sum()).item()  # the program's own work between replays
+
+
+def test_a_decoding_loop_of_replays(ds):  # noqa: F811
+    import synth
+    from draft_sampling_verification_markov_amd import runner
+    cfg = synth.get_config("tbias").replace(B=5, K=4, V=1024, seed=12)
+    P = ds.Problem.from_config(cfg)
+    B, K, Hq, Hkv, D = 5, 4, 8, 2, 64
+    C = ds.Cache.make(B, 12, 16, 2, 1, Hq, Hkv, D)
+    gen = torch.Generator(device="cuda").manual_seed(81)
+    book = torch.randn((cfg.V, Hkv + Hq, D), device="cuda", generator=gen).bfloat16()
+
+    class Loop:
+        def __init__(self):
+            self.x = runner.CycleInputs.upload(synth.make_inputs(cfg), "cuda")
+            self.o, self.cache = runner.CycleOutputs(P), runner.PagedCache(C, K + 1)
+            self.out = torch.zeros(B * (K + 1), Hq, D, dtype=torch.bfloat16, device="cuda")
+
+        def forward(self, tok, n_new):
+            row = book[tok.long()].view(B * (K + 1), Hkv + Hq, D)
+            self.cache.append(0, row[:, :Hkv], row[:, :Hkv], n_new)
+            self.cache.attend(0, row[:, Hkv:], self.out, n_new=n_new)
+
+        def cycle(self):
+            n_new = runner.run_cached_cycle(P, self.x, self.o, self.cache, self.forward, path=ds.DRAFT_PER_POSITION)
+            self.x.anchor.copy_(self.o.next_anchor)
+            return n_new
+
+        def state(self):
+            o, c = self.o, self.cache
+            return [o.tok, o.n_sched, o.out_tok, o.n_acc, o.next_anchor, c.table, c.length, c.ref, c.n_short, self.out, c.k,
+                    c.v]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Loop().cycle()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    eager, graphed = Loop(), Loop()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rows = graphed.cycle()
+    ended = 0
+    for i in range(14):
+        print(f"[gpu] decoding loop, replay {i}", flush=True)
+        g.replay()
+        n_new = eager.cycle()
+        torch.cuda.synchronize()
+        assert torch.equal(rows, n_new), i
+        for j, (a, b) in enumerate(zip(graphed.state(), eager.state())):
+            assert torch.equal(a, b), (i, j)
+        ended += int((n_new == 0).sum())
+        assert (n_new > 0).any() or i > 4
+    assert ended and (eager.cache.length <= 32).all()
