@@ -3,10 +3,11 @@
 Each ``csrc/*.hip`` translation unit is compiled to an object in parallel and
 the objects are linked into ``libdspark.so`` next to this file.  The ABI unit is
 compiled a second time with DSPARK_DEBUG_CHECKS and linked with the same kernel
-objects into ``libdspark_debug.so`` (input and output scans around every call).
-Both link the roctx library (one range per ABI call).  Packed-FP32 instructions
-are disabled for device code (the flag is a device feature; the host pass prints
-a harmless "not a recognized feature" warning).
+objects into ``libdspark_debug.so`` (input and output scans around every call of
+dspark.h; the paged cache's calls are the same in both libraries).  Both link the
+roctx library (one range per ABI call).  Packed-FP32 instructions are disabled for
+device code (the flag is a device feature; the host pass prints a harmless "not a
+recognized feature" warning).
 """
 from __future__ import annotations
 

@@ -89,8 +89,8 @@ dspark_status dspark_probe_draws(uint64_t seed, const uint32_t* ctr, int32_t n, 
 
 /*
  * Debug checks.  The library built with DSPARK_DEBUG_CHECKS (libdspark_debug.so)
- * scans every call's inputs before its kernels and its outputs after them with
- * kernels of its own, on `stream`, and raises bits of a per-device flag word
+ * scans the inputs of every call of dspark.h before its kernels and its outputs after
+ * them with kernels of its own, on `stream`, and raises bits of a per-device flag word
  * (never a trap; the call's results are those of the ordinary library, which
  * these scans do not touch):
  *   DSPARK_DEBUG_LOGITS          a non-finite base or target logit (NaN or infinity)
@@ -108,6 +108,8 @@ dspark_status dspark_probe_draws(uint64_t seed, const uint32_t* ctr, int32_t n, 
  *                                (its results are then unspecified)
  * dspark.h leaves calls on inputs that break its contract undefined; these flags
  * report them.  The ordinary library returns DSPARK_E_UNSUPPORTED from both calls.
+ * The calls of dspark_cache.h have no scans: what they read on the device is clamped
+ * or left out as that header says, in both libraries.
  */
 enum {
   DSPARK_DEBUG_LOGITS = 1,
