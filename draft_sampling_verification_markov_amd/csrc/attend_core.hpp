@@ -13,8 +13,8 @@
 // (key_of_row): the product sums over keys, so their order within the tile is free.
 //
 // Running maximum.  m only moves when some row's maximum rises by more than 2^8 in
-// weight; until then P may reach 2^8, which costs no precision (fp32 sums, and bf16
-// rounds relative to the value), and O is not rescaled.
+// weight; until then P may reach 2^8, which costs no precision (fp32 sums, and a rounding
+// to bf16 is relative to the value), and O is not rescaled.
 //
 // What a row does not see must not reach it, not even as NaN times a weight of 0.
 // Scores are replaced before the exponential.  In the tiles that some rows see in part

@@ -10,6 +10,11 @@
 // Measured: 256 tokens over up to 4096 keys, 8 heads of 128, bf16 (2.37 GB) 375 us, 6.3 TB/s;
 // 2 tokens over up to 200,000 keys, 4 heads of 128, e4m3 (318 MB) 55 us and 5 for the join.
 //
+// Weights: the product with bf16 values takes a weight in two bf16 terms, the rounded one
+// and the rest (2^-16 of the weight is lost, not 2^-8).  The matrix units wait for memory
+// here, so the second product costs next to nothing: 256 tokens over up to 4096 keys bf16
+// 373.8 -> 374.2 us, 2 over up to 200,000 e4m3 59.5 -> 60.3.
+//
 // A tile of keys is two S^T tiles of 16 keys x 16 rows, for fp32 one (two need twice the
 // registers of K and V: 64 tokens over 4000 keys, head size 128, 148 -> 106 us; head size
 // 256, where they spill, a few hundred keys 37 -> 21).  With lane l = 16 g + c (c < 16):
@@ -271,18 +276,25 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
               for (int db = 0; db < TT::kBlocks; ++db)
                 acc[nb][db] = mma16(lane4(v[db], e), w[nb][0][e], acc[nb][db]);
           } else {
-            bf16x8_t pw;
+            bf16x8_t pw, rest;  // the weights in bf16, and what that leaves of them
 #pragma unroll
             for (int t = 0; t < TT::kS; ++t)
 #pragma unroll
               for (int i = 0; i < 4; i += 2) {
-                const bf16x2_t x = __builtin_convertvector(f32x2_t{w[nb][t][i], w[nb][t][i + 1]}, bf16x2_t);
-                pw[4 * t + i] = x[0];
-                pw[4 * t + i + 1] = x[1];
+                const f32x2_t x{w[nb][t][i], w[nb][t][i + 1]};
+                const bf16x2_t y = __builtin_convertvector(x, bf16x2_t);
+                const bf16x2_t z = __builtin_convertvector(f32x2_t{x[0] - (float)y[0], x[1] - (float)y[1]}, bf16x2_t);
+                pw[4 * t + i] = y[0];
+                pw[4 * t + i + 1] = y[1];
+                rest[4 * t + i] = z[0];
+                rest[4 * t + i + 1] = z[1];
               }
 #pragma unroll
-            for (int db = 0; db < TT::kBlocks; ++db)
-              acc[nb][db] = mma16(value_operand<CT>(v[db]), pw, acc[nb][db]);
+            for (int db = 0; db < TT::kBlocks; ++db) {
+              const bf16x8_t x = value_operand<CT>(v[db]);
+              acc[nb][db] = mma16(x, pw, acc[nb][db]);
+              acc[nb][db] = mma16(x, rest, acc[nb][db]);
+            }
           }
         }
     }

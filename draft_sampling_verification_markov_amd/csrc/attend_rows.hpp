@@ -10,6 +10,11 @@
 // rows a wave 1272, for the moves between its registers); 256 x up to 17 tokens over up to
 // 2048 keys (0.98 GB) 183 us, 5.4 TB/s.
 //
+// Weights are rounded to bf16 for their product with the values (half a step, 2^-8 of a
+// weight; sums, maxima and results stay fp32): in two terms, as k_attend_keys takes them,
+// the second product doubles, and the prompt takes 765 us in place of 563, the 256 x up to
+// 17 tokens 188 for 184, with e4m3 values 145 for 126.
+//
 // A tile of kKeys keys and values comes by LDS DMA (16 bytes a lane) into one of two
 // buffers while the other is used; the buffers are distinct __shared__ objects, so that
 // the compiler lets reads of one pass the DMA into the other.

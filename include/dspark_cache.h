@@ -118,8 +118,9 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  * Outputs: out [n_rows][Hq][D] (rows out_stride elements apart); lse
  *          [n_rows][Hq] fp32 or NULL.  Rows that belong to no request are left as
  *          they were.  Outputs must not overlap the inputs or each other.
- * Products and sums are fp32; with bf16 data the softmax weights are rounded to
- * bf16 for their product with the values.  causal = 0 is the mask of a parallel
+ * Products and sums are fp32.  With bf16 data the softmax weights enter their product
+ * with the values in two bf16 terms (2^-16 relative) where max_new * Hq / Hkv <= 16, and
+ * rounded to bf16 (2^-8) beyond, where products are what a call waits for.  causal = 0 is the mask of a parallel
  * drafter's block.  n_rows = 0 does nothing.
  */
 dspark_status dspark_cache_attend(const dspark_cache* C, int32_t layer, const void* q, int64_t q_stride, int32_t n_rows,
