@@ -31,12 +31,16 @@ struct Rule {
   long long whole;  // segments
   long long twice;  // keys of all segments
 };
+// Keys that a request can see, from what the host knows: its row of the page table, or the window.
+long long most_keys(const dspark_cache& C, int32_t max_new, int window) {
+  const long long row = (long long)C.max_pages * C.page, seen = (long long)window + max_new;
+  return window > 0 && seen < row ? seen : row;
+}
 Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int per_cu, const Rule& r) {
   Split pl{};
   pl.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
   pl.unit_shift = unit_shift;
-  long long keys = (long long)C.max_pages * C.page;
-  if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
+  const long long keys = most_keys(C, max_new, window);
   const long long segments = (long long)C.B * pl.row_tiles * C.Hkv;
   const bool direct = segments <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
                                                 (pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
@@ -48,9 +52,13 @@ Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int
 // Keys that one workgroup reads, and that the 256 MB last-level cache does not hold until
 // the next call, are read with the streaming policy: 256 requests x 17 rows 191 -> 182 us,
 // 256 x 1 402 -> 374.  For others it costs: prompts, whose row tiles meet in L2, 563 -> 589,
-// 64 tokens over 2000 keys x 2 heads (72 MB) 27.8 -> 29.6.
-bool read_once(const dspark_cache& C, const Split& pl) {
-  return pl.row_tiles == 1 && 2 * page_bytes(C) * C.n_pages > ((size_t)256 << 20);
+// 64 tokens over 2000 keys x 2 heads (72 MB) 27.8 -> 29.6, a window of 512 keys of 64
+// requests x 8 heads in a pool of 2 GB 25.9 -> 27.9.  How much a call reads at most, from
+// what the host knows: the pool, or what its requests can see.
+bool read_once(const dspark_cache& C, const Split& pl, int32_t max_new, int window) {
+  const size_t page = 2 * page_bytes(C), pool = page * C.n_pages;
+  const size_t seen = page / C.page * C.B * (size_t)most_keys(C, max_new, window);
+  return pl.row_tiles == 1 && (seen < pool ? seen : pool) > ((size_t)256 << 20);
 }
 
 template <int CT, int D, int ROWS, typename Kernel>
@@ -80,7 +88,7 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
                   NB == 1 ? 1 << 22 : 1 << 20};
   const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC, rule);
   return run_plan<CT, D, NB * 16>(
-      C, a, pl, read_once(C, pl) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
+      C, a, pl, read_once(C, pl, a.c.max_new, a.window) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
 
 template <int CT, int D>
@@ -90,7 +98,7 @@ hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   // 159 / 115
   constexpr Rule kRule{kFewKeys, 2 * kCUs, 1 << 20};
   const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, 2, kRule);
-  return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
+  return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl, a.c.max_new, a.window) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 
 // Workgroups of k_attend_keys that a CU holds, by their registers.
