@@ -528,7 +528,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
   const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
   auto slot = [&](int i) __attribute__((always_inline)) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };
   auto weight = [](float m, float top) __attribute__((always_inline)) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
-  auto share = [](float m, float l, float f) __attribute__((always_inline)) { return m == -INFINITY ? l : l * f; };  // (such an l is 0 or NaN)
+  // (the l of such an m is 0 or NaN)
+  auto share = [](float m, float l, float f) __attribute__((always_inline)) { return m == -INFINITY ? l : l * f; };
   auto add = [](float4& o, const float4& x, float f) __attribute__((always_inline)) {
     o.x = fmaf(x.x, f, o.x);
     o.y = fmaf(x.y, f, o.y);

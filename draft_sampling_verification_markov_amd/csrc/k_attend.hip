@@ -23,6 +23,11 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // the longest requests go first (100 requests of up to 17 rows over up to 3000 keys 103 ->
 // 78 us, 256 over 2048 192 -> 184, 8 x 300 rows fp32 over 2000 279 -> 230); each workgroup
 // counts out its request, about 1 us, so not for few keys, nor with a window.
+// The host knows no lengths: a segment's keys are what its request's row of the page table
+// (or the window) holds, its rows what max_new allows.  Short requests in a long table are
+// dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows
+// over 1000 52.0 / 53.4), and one prompt of 2048 rows among 255 tokens has the row tiles of
+// all of them launched (1957 us; in calls of their own 121 + 391).
 // Dealt ones go to one worker a CU, or to two where there are enough keys (`twice`): the
 // second hides the other's waits, but doubles the partial results and halves their shares.
 constexpr int kFewKeys = 1024, kSomeKeys = 4096;
@@ -76,10 +81,11 @@ hipError_t run_plan(const dspark_cache& C, const AttendArgs& a, Split pl, Kernel
 template <int CT, int D, int NB, int OCC>
 hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   // `few`: wide fp32 products make the loop longer: 32 segments of 1000 keys, head size 256,
-  // 46 us whole, 24 dealt, but 512 segments of 900 keys 121 / 126, head size 128 61 / 72.  `twice`: for a few rows (memory bound) one worker a CU suffices
-  // for long: a token over 20000 keys 15.9 us with one, 18.8 with two, 3 requests over
-  // 150000 keys x 4 heads 108 / 111, 200 over 3000 x 8 heads 250 / 244; for more rows, 608
-  // segments of 3000 keys, 133 / 111.
+  // 46 us whole, 24 dealt, but 512 segments of 900 keys 121 / 126, head size 128 61 / 72.
+  // `twice`: for a few rows (memory bound) one worker a CU suffices for long: a token over
+  // 20000 keys 15.9 us with one, 18.8 with two, 3 requests over 150000 keys x 4 heads
+  // 108 / 111, 200 over 3000 x 8 heads 250 / 244; for more rows, 608 segments of 3000 keys,
+  // 133 / 111.
   // `whole`: as many as the chip holds, where the longest go first (256 tokens over up to
   // 4096 keys x 8 heads 375 us whole, 402 dealt; 256 over 2000 x 4, e4m3, 58 / 84); many more
   // where they cannot be ordered.

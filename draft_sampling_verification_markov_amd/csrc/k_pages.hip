@@ -7,7 +7,7 @@
 // or atomics run (sums of references, ranks from prefix sums, lowest free ids
 // first).  Device-wide dependencies are launch boundaries: a launch of the next
 // kernel costs about 2 us on the stream, a grid barrier over 8 XCDs no less.  An update of
-// 256 slots and 17,088 pages takes 2.5 + 2.6 + 3.0 + 4.5 + 3.3 us in its five kernels.
+// 256 slots and 68,125 pages takes 2.5 + 2.4 + 3.0 + 4.4 + 3.2 us in its five kernels.
 #include <type_traits>
 
 #include "dspark_cache_internal.hpp"
@@ -28,12 +28,14 @@ __device__ __forceinline__ uint32_t f8_pair(float x, float y) {
 // A workgroup writes 8-token groups (the v_pool's unit [D][8]) of a few heads, D / 2
 // threads each.  Values: a thread carries 2 coordinates, reads 8 rows (neighbouring
 // threads neighbouring coordinates) and writes 2 x 8 tokens as whole 16-byte pieces; of
-// a group that is new in part it reads the old pieces too and merges, since 2-byte
-// stores cost more (256 x 17 rows of 8 x 128, bf16, 13.6 us with them, 8.4 so).  Keys: rows copied in 16-byte
-// pieces.  All loads are issued before the first use.  Bound by the bytes of the new
-// rows; for a few tokens by the latency of length -> table -> rows -> store; with an e4m3
-// cache by the exact divisions (8192 rows of 8 x 128, 50 MB: 15.6 us; a reciprocal and
-// its correction took as long).
+// a group that is new in part it merges with the old pieces (read for every group), since
+// 2-byte stores cost more (256 x 17 rows of 8 x 128, bf16, 13.6 us with them, 8.4 so).
+// Keys: rows copied in 16-byte pieces.  All loads are issued before the first use.  Bound
+// by memory and the way to it, length -> table -> rows and old values -> store: of those
+// 8.4 us the waves wait 59% (25 MB read and written), of the 15.6 of 8192 rows of 8 x 128
+// into an e4m3 cache 33%, and 41% for the issue of an instruction (59 MB, 8 of them old
+// values; a reciprocal with a correction in place of the divisions gained nothing, vector
+// instructions issue in 17% of the waves' cycles).
 template <int CT>
 struct CacheType;
 template <>

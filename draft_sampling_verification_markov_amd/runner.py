@@ -108,7 +108,8 @@ class PagedCache:
     """Pools, page tables, lengths and references of a paged cache, and its calls.
 
     table, length and ref are the present sequences; update writes the other set of
-    them and swaps the two (so a captured graph holds an even number of updates)."""
+    them and swaps the two, compact those of table and ref (so a captured graph holds an even
+    number of updates, and of compactions)."""
 
     def __init__(self, C: dspark.Cache, max_new: int, device="cuda", k_scale=None, v_scale=None):
         self.C, self.max_new = C, int(max_new)

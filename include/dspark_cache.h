@@ -114,7 +114,7 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  *
  * Inputs:  q [n_rows][Hq][D] (data_dtype, rows q_stride elements apart, a multiple
  *          of 16 bytes); n_new, row_start, length, table, k_scale, v_scale as above;
- *          scale > 0, scale * log2(e) finite.
+ *          scale > 0, scale * log2(e) finite (with an e4m3 cache also times k_scale).
  * Outputs: out [n_rows][Hq][D] (rows out_stride elements apart); lse
  *          [n_rows][Hq] fp32 or NULL.  Rows that belong to no request are left as
  *          they were.  Outputs must not overlap the inputs or each other.
@@ -122,6 +122,10 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  * with the values in two bf16 terms (2^-16 relative) where max_new * Hq / Hkv <= 16, and
  * rounded to bf16 (2^-8) beyond, where products are what a call waits for.  causal = 0 is the mask of a parallel
  * drafter's block.  n_rows = 0 does nothing.
+ * Work is launched for max_new rows of all B slots and for the width of the page
+ * table, whatever n_new and length hold: prompts are better in a call over their own
+ * slots (a dspark_cache of fewer B, table and length from the first of them on), single
+ * tokens in one with a small max_new, where the prompts' n_new is 0.
  */
 dspark_status dspark_cache_attend(const dspark_cache* C, int32_t layer, const void* q, int64_t q_stride, int32_t n_rows,
                                   const int32_t* n_new, const int32_t* row_start, int32_t max_new,
@@ -161,6 +165,9 @@ dspark_status dspark_cache_update(const dspark_cache* C, const int32_t* parent, 
  * dspark_cache_compact -- with n_live pages in use, those with ids >= n_live move
  * (all layers, both pools) to the free ids below n_live, both in ascending order,
  * so that the pool's first n_live pages are the live ones.  Lengths do not change.
+ * A caller that wants a smaller pool copies the first n_live (or more) pages of every
+ * layer of both pools into it, and goes on with the same table and the first entries
+ * of ref, under a dspark_cache with that n_pages; the same pages are a snapshot's.
  *
  * Inputs:  table [B][max_pages], length [B], ref [n_pages].
  * Outputs: table_out (entries past a sequence's pages, and ids that ref calls free,
