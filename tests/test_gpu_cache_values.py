@@ -117,3 +117,19 @@ def test_a_value_reaches_the_rows_that_see_it(ds, dtype, rows, G, causal, window
         want.view(B, rows, G, 64)[torch.from_numpy(sees)[..., None].expand(-1, -1, G)].index_fill(1, torch.tensor([7]), float("nan"))
     torch.testing.assert_close(out, want, rtol=0, atol=0, equal_nan=True)
     assert torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "f8"])
+@pytest.mark.parametrize("rows,G", [(5, 3), (40, 2)])
+@pytest.mark.parametrize("width", [None, 100])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_a_query_row_stays_by_itself(ds, dtype, rows, G, width, bad):  # noqa: F811
+    # one head of one row of q is not finite: that result is NaN (or empty), all others are as without it
+    c = cu.make(63, dtype, PAGE, 64, 2 * G, 2, [rows, 2], [300 + rows, 50], width=width)
+    ref = gpu_attend(ds, c)
+    c.q[rows // 2, 1] = float(bad)
+    out, lse = gpu_attend(ds, c)
+    keep = torch.ones(out.shape[:2], dtype=torch.bool)
+    keep[rows // 2, 1] = False
+    assert torch.equal(out[keep], ref[0][keep]) and torch.equal(lse[keep], ref[1][keep])
+    assert torch.isnan(out[rows // 2, 1]).all()
