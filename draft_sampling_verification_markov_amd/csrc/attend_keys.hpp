@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
         uint32_t bits = 0;
 #pragma unroll
         for (int db = 0; db < TT::kBlocks; ++db) find_nonfinite<CT>(v[db], bits);
-        if (__any(bits & kOdd<CT>)) {
+        if (__builtin_expect(__any(bits & kOdd<CT>), 0)) {
           odd = 1;
 #pragma unroll
           for (int db = 0; db < TT::kBlocks; ++db) v[db] = finite_part<CT>(v[db]);
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
           const float4 o0 = so[0][d4][r], o1 = so[1][d4][r], o2 = so[2][d4][r], o3 = so[3][d4][r];
           float4 y = make_float4(o0.x + o1.x + o2.x + o3.x, o0.y + o1.y + o2.y + o3.y, o0.z + o1.z + o2.z + o3.z,
                                  o0.w + o1.w + o2.w + o3.w);
-          if (odd) {
+          if (__builtin_expect(odd, 0)) {
             const int pos = g.pos0 + (g.row0 + rho) / G;
             add_nonfinite<CT, D, TT::kKeys>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
           }

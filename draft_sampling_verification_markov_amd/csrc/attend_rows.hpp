@@ -316,16 +316,17 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
         uint32_t bits = 0;
 #pragma unroll
         for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i) find_nonfinite<CT>(mine[i * kAttendThreads], bits);
-        if (__any(bits & kOdd<CT>)) {
+        if (__builtin_expect(__any(bits & kOdd<CT>), 0)) {  // word by word, for few registers
+          uint32_t seen = 0;
 #pragma unroll 1
-          for (int i = 0; i < S::kBytes / 16 / kAttendThreads; ++i) {
-            const int group = (threadIdx.x + i * kAttendThreads) * 16 / (8 * D * kEs);  // of 8 keys
-            const uint4 x = mine[i * kAttendThreads];
-            uint32_t seen = 0;
-            find_nonfinite<CT>(KeysWithin<CT, uint4>(key0 + 8 * group, g.lo, g.hi).of(x), seen);
-            if (seen & kOdd<CT>) odd = 1;
-            mine[i * kAttendThreads] = finite_part<CT>(x);
+          for (int i = 0; i < S::kBytes / 4 / kAttendThreads; ++i) {
+            const int at = 4 * (threadIdx.x + (i >> 2) * kAttendThreads) + (i & 3);  // 8 tokens are 2 kEs words
+            uint32_t* const word = reinterpret_cast<uint32_t*>(vb) + at;
+            const int key = key0 + at / (2 * kEs * D) * 8 + at % (2 * kEs) * (4 / kEs);
+            find_nonfinite<CT>(*word & keys_within<CT>(key, g.lo, g.hi), seen);
+            *word = finite_word<CT>(*word);
           }
+          if (seen & kOdd<CT>) odd = 1;
         }
         barrier_lds_only();
       }
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
           else if (r >= 0)
             store4<CT>(a.out, r * a.out_stride + (size_t)hq * D + d, y);
         }
-      if (any_odd && !none) {
+      if (__builtin_expect(any_odd && !none, 0)) {
         const int pos = g.pos0 + (g.row0 + rho) / G;
 #pragma unroll 1
         for (int d = 4 * h; d < D; d += 8) {

@@ -93,8 +93,9 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   const Rule rule{CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys, C.B <= kAttendThreads ? kHeld : 16 * kHeld,
                   NB == 1 ? 1 << 22 : 1 << 20};
   const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC, rule);
+  const bool once = read_once(C, pl, a.c.max_new, a.window);
   return run_plan<CT, D, NB * 16>(
-      C, a, pl, read_once(C, pl, a.c.max_new, a.window) ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
+      C, a, pl, once ? k_attend_keys<CT, D, NB, OCC, NB == 1> : k_attend_keys<CT, D, NB, OCC, false>, s);
 }
 
 template <int CT, int D>
@@ -104,7 +105,8 @@ hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   // 159 / 115
   constexpr Rule kRule{kFewKeys, 2 * kCUs, 1 << 20};
   const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, 2, kRule);
-  return run_plan<CT, D, S::kRows>(C, a, pl, read_once(C, pl, a.c.max_new, a.window) ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
+  const bool once = read_once(C, pl, a.c.max_new, a.window);
+  return run_plan<CT, D, S::kRows>(C, a, pl, once ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 
 // Workgroups of k_attend_keys that a CU holds, by their registers.

@@ -120,8 +120,8 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  *          they were.  Outputs must not overlap the inputs or each other.
  * Products and sums are fp32.  With bf16 data the softmax weights enter their product
  * with the values in two bf16 terms (2^-16 relative) where max_new * Hq / Hkv <= 16, and
- * rounded to bf16 (2^-8) beyond, where products are what a call waits for.  causal = 0 is the mask of a parallel
- * drafter's block.  n_rows = 0 does nothing.
+ * rounded to bf16 (2^-8) beyond, where products are what a call waits for.  causal = 0 is
+ * the mask of a parallel drafter's block.  n_rows = 0 does nothing.
  * Work is launched for max_new rows of all B slots and for the width of the page
  * table, whatever n_new and length hold: prompts are better in a call over their own
  * slots (a dspark_cache of fewer B, table and length from the first of them on), single
