@@ -21,7 +21,8 @@
 // or not at all (the sequence's end, the diagonal, a window's edge) values that are not
 // finite are replaced by 0; if a row does see one, the coordinate's result is made NaN
 // or infinite when it is stored (add_nonfinite), from the values themselves, by a walk over
-// the keys of these tiles.  One that no row sees (behind the sequence's end) costs no walk.
+// the keys of these tiles.  One that no row sees (behind the sequence's end) starts no walk
+// in the row kernel; in the other the walk is short, and a check would cost registers.
 // All other tiles are seen whole by all rows and need no such care.  These branches are
 // marked as unlikely: without that their code costs the loops registers (256 x up to 17
 // tokens over up to 2048 keys fp32 562 us, with it 517).
