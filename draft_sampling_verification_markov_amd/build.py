@@ -4,7 +4,7 @@ Each ``csrc/*.hip`` translation unit is compiled to an object in parallel and
 the objects are linked into ``libdspark.so`` next to this file.  The ABI unit is
 compiled a second time with DSPARK_DEBUG_CHECKS and linked with the same kernel
 objects into ``libdspark_debug.so`` (input and output scans around every call of
-dspark.h; the paged cache's calls are the same in both libraries).  Both link the
+dspark.h; the calls of the paged cache and of trees are the same in both libraries).  Both link the
 roctx library (one range per ABI call).  Packed-FP32 instructions are disabled for
 device code (the flag is a device feature; the host pass prints a harmless "not a
 recognized feature" warning).
@@ -40,6 +40,7 @@ CFLAGS = [
 SOURCE_FLAGS = {
     "k_persist.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "k_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "k_attend_tree.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -76,7 +76,11 @@ struct Masks {
   __device__ __forceinline__ int lo(int pos) const { return window > 0 ? max(0, pos - window + 1) : 0; }
 };
 
-template <int ROWS>
+// The new tokens may be the nodes of a tree (TREE): a node sees its context, the positions
+// before the new tokens, within the window of its depth, and of the nodes up to itself those
+// of its bits.  What every row of a tile sees is then context: depths lie between 0 and the
+// node's number.
+template <int ROWS, bool TREE>
 __device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int b, int rt) {
   Geometry g;
   const int G = a.c.Hq / a.c.Hkv;
@@ -94,12 +98,50 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p
   const Masks m{a.causal, a.window, len};
   const int first = g.pos0 + g.row0 / G, last = g.pos0 + (g.row0 + g.rows - 1) / G;
   g.hi = m.hi(last);
-  g.lo = min(m.lo(first), g.hi);
-  g.all_hi = m.hi(first);
+  g.lo = min(m.lo(TREE ? g.pos0 : first), g.hi);
+  g.all_hi = TREE ? max(0, g.pos0) : m.hi(first);
   g.all_lo = m.lo(last);
   g.tile0 = g.lo >> p.unit_shift;
   g.tiles = max(1, ((g.hi + (1 << p.unit_shift) - 1) >> p.unit_shift) - g.tile0);  // 1: its rows are written
   return g;
+}
+
+// The keys that a row sees: all in [lo, hi), of a tree's nodes those of its bits.
+template <bool TREE>
+struct RowKeys {
+  int lo, hi;
+};
+template <>
+struct RowKeys<true> {
+  int lo, hi;
+  const uint32_t* bits;  // of its row of the mask; null for a row that is not there
+};
+// Token t of a request, whose row of q is r (-1: none).
+template <bool TREE>
+__device__ __forceinline__ RowKeys<TREE> row_keys(const AttendArgs& a, const Geometry& g, const Masks& m, int t, long long r) {
+  RowKeys<TREE> k;
+  if constexpr (TREE) {
+    const int depth = a.depth && r >= 0 ? min(max(a.depth[r], 0), t) : 0;
+    k.lo = min(m.lo(g.pos0 + depth), max(0, g.pos0));
+    k.hi = m.hi(g.pos0 + t);
+    k.bits = r >= 0 ? a.mask + r * a.mask_words : nullptr;
+  } else {
+    k.lo = m.lo(g.pos0 + t);
+    k.hi = m.hi(g.pos0 + t);
+  }
+  return k;
+}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Which of the 32 keys from key0 on a tree's row sees.  A row that is not there sees all
+// (its results are left out at the end).
+__device__ __forceinline__ uint32_t tree_seen(const AttendArgs& a, const Geometry& g, const RowKeys<true>& k, int key0) {
+  if (!k.bits) return ~0u;
+  const int node = key0 - g.pos0, w = node >> 5;  // of key0
+  const uint32_t w0 = (unsigned)w < (unsigned)a.mask_words ? k.bits[w] : 0u;
+  const uint32_t w1 = (unsigned)(w + 1) < (unsigned)a.mask_words ? k.bits[w + 1] : 0u;
+  const uint32_t nodes = (uint32_t)(((uint64_t)w1 << 32 | w0) >> (node & 31));
+  const uint32_t context = low_bits(-node) & ~low_bits(k.lo - key0);
+  return context | (nodes & low_bits(k.hi - key0));
 }
 
 // Position in the dealt work: the segment that holds a worker's first unit.
@@ -138,14 +180,14 @@ __device__ __forceinline__ int wg_prefix(int v, int* sh, int& all) {
 // chunk at a time, one a thread; the request is the last one whose units begin at or before the
 // worker's, and within it the head and then the row tile follow.  For the batches that
 // are dealt (up to a few thousand pairs) that is cheaper than a launch of its own.
-template <int ROWS, int THREADS>
+template <int ROWS, int THREADS, bool TREE>
 __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p, int worker, int* sh) {
   const int RT = p.row_tiles, Hkv = a.c.Hkv;
   const long long pairs = (long long)a.c.B * RT;
   __shared__ int found_b, found_rt, found_skip;
   __shared__ long long found_before;
   auto tiles_of = [&](long long i) __attribute__((always_inline)) {
-    return i < pairs ? geometry<ROWS>(a, p, RT == 1 ? (int)i : (int)(i / RT), RT == 1 ? 0 : (int)(i % RT)).tiles : 0;
+    return i < pairs ? geometry<ROWS, TREE>(a, p, RT == 1 ? (int)i : (int)(i / RT), RT == 1 ? 0 : (int)(i % RT)).tiles : 0;
   };
   Start s{};
   long long total = 0;
@@ -182,21 +224,21 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   s.b = found_b;
   long long in = s.unit - found_before * Hkv;  // units into the request
   if (RT == 1) {
-    const int t = geometry<ROWS>(a, p, s.b, 0).tiles;
+    const int t = geometry<ROWS, TREE>(a, p, s.b, 0).tiles;
     s.head = (int)(in / t);
     s.skip = (int)(in % t);
     return s;
   }
   long long per_head = 0;
   for (int c = 0; c < RT; c += THREADS) {
-    mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
+    mine = c + (int)threadIdx.x < RT ? geometry<ROWS, TREE>(a, p, s.b, c + threadIdx.x).tiles : 0;
     wg_prefix<THREADS>(mine, sh, all);
     per_head += all;
   }
   s.head = (int)(in / per_head);
   in %= per_head;
   for (int c = 0; c < RT; c += THREADS) {
-    if (RT > THREADS) mine = c + (int)threadIdx.x < RT ? geometry<ROWS>(a, p, s.b, c + threadIdx.x).tiles : 0;
+    if (RT > THREADS) mine = c + (int)threadIdx.x < RT ? geometry<ROWS, TREE>(a, p, s.b, c + threadIdx.x).tiles : 0;
     const int ahead = wg_prefix<THREADS>(mine, sh, all);
     if (mine > 0 && in >= ahead && in < ahead + mine) {
       found_rt = c + threadIdx.x;
@@ -260,13 +302,13 @@ inline int whole_grid(const dspark_cache& C, Split& p) {
 }
 
 // The next segment that has units (there is one).
-template <int ROWS>
+template <int ROWS, bool TREE>
 __device__ __forceinline__ Geometry next_segment(const AttendArgs& a, const Split& p, Start& s) {
   s.skip = 0;
   ++s.row_tile;
   while (true) {
     Geometry g;
-    if (s.row_tile < p.row_tiles && (g = geometry<ROWS>(a, p, s.b, s.row_tile)).tiles > 0) return g;
+    if (s.row_tile < p.row_tiles && (g = geometry<ROWS, TREE>(a, p, s.b, s.row_tile)).tiles > 0) return g;
     // the request's row tiles are done (or it has none): its next head, or the next request
     if (s.row_tile > 0 && ++s.head < a.c.Hkv) {
       s.row_tile = 0;
@@ -290,14 +332,39 @@ struct TableRow {
 
 // ---- operands
 // Element types of the two products: bf16 MFMA for bf16 and e4m3 caches (an e4m3
-// value is a bf16 value; its scale is a factor of the scores and of the result),
-// fp32 MFMA for fp32.
+// value is a bf16 value; its scale is a factor of the scores and of the result, or, with a
+// scale a token, of the token's scores and of its weights next to the values), fp32 MFMA
+// for fp32.
 template <int CT>
 struct Operand {
   static constexpr bool kF32 = CT == DSPARK_F32;
   static constexpr int kBytes = CT == DSPARK_F32 ? 4 : CT == DSPARK_BF16 ? 2 : 1;
+  static constexpr bool kToken = CT == DSPARK_F8E4M3_TOKEN;
   using Data = typename std::conditional<kF32, float, uint16_t>::type;
 };
+
+// First byte of a token's key in a layer's pool, and of 8 tokens' values: `off` is the
+// token's place in page `id`, for values a multiple of 8.
+template <int CT, int D>
+__device__ __forceinline__ size_t token_at(const CacheView& c, unsigned id, int head, int off) {
+  constexpr int kBytes = D * Operand<CT>::kBytes;
+  const size_t block = (size_t)(id * (unsigned)c.Hkv + head) << c.page_shift;
+  if constexpr (Operand<CT>::kToken)
+    return block * (kBytes + scale_bytes(CT)) + off * kBytes;
+  else
+    return (block + off) * kBytes;
+}
+// First byte of the token's scale, which follows the page's entries of the head.
+template <int D>
+__device__ __forceinline__ size_t scale_at(const CacheView& c, unsigned id, int head, int off) {
+  const size_t block = (size_t)(id * (unsigned)c.Hkv + head) << c.page_shift;
+  return block * (D + 4) + ((size_t)D << c.page_shift) + off * 4;
+}
+// A scale that belongs to no token may be anything.
+__device__ __forceinline__ float finite_scale(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
+__device__ __forceinline__ float4 finite_scales(float4 x) {
+  return make_float4(finite_scale(x.x), finite_scale(x.y), finite_scale(x.z), finite_scale(x.w));
+}
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint4 w) { return __builtin_bit_cast(bf16x8_t, w); }
 __device__ __forceinline__ bf16x8_t f8_to_bf16x8(uint32_t lo, uint32_t hi) {
@@ -414,16 +481,16 @@ __device__ __forceinline__ float cached(const char* p) {
     return __builtin_amdgcn_cvt_f32_fp8(*reinterpret_cast<const uint8_t*>(p), 0);
 }
 
-// What the values that are not finite make of coordinates d .. d + 3 of the row at
-// position pos: those of the keys in [k0, k1) that it sees, in tiles of TILE keys that
-// are not wholly in [all_lo, all_hi) (the others' products took them as they are).  A walk
-// over groups of 8 keys, whose values of 4 coordinates lie together.
-template <int CT, int D, int TILE>
-__device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometry& g, const Masks& mask, int head,
-                                              int pos, int d, int k0, int k1, float4& y) {
+// What the values that are not finite make of coordinates d .. d + 3 of a row: those of
+// the keys in [k0, k1) that it sees, in tiles of TILE keys that are not wholly in [all_lo,
+// all_hi) (the others' products took them as they are).  A walk over groups of 8 keys, whose
+// values of 4 coordinates lie together.
+template <int CT, int D, int TILE, bool TREE>
+__device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometry& g, const RowKeys<TREE>& keys, int head,
+                                              int d, int k0, int k1, float4& y) {
   constexpr int kEs = Operand<CT>::kBytes;
   const CacheView& c = a.c;
-  const int lo = max(k0, mask.lo(pos)), hi = min(k1, mask.hi(pos));
+  const int lo = max(k0, keys.lo), hi = min(k1, keys.hi);
   const int whole0 = (g.all_lo + TILE - 1) & ~(TILE - 1), whole1 = g.all_hi & ~(TILE - 1);  // the others' tiles
   for (int j0 = lo & ~7; j0 < hi; j0 += 8) {
     if (j0 >= whole0 && j0 < whole1) {
@@ -431,8 +498,8 @@ __device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometr
       continue;
     }
     const unsigned page = min((unsigned)c.table[(size_t)g.b * c.max_pages + (j0 >> c.page_shift)], (unsigned)c.n_pages - 1u);
-    const size_t token = (((size_t)page * c.Hkv + head) << c.page_shift) + (j0 & ((1 << c.page_shift) - 1));
-    const char* src = static_cast<const char*>(a.v_pool) + (token * D + (size_t)d * 8) * kEs;
+    const char* src = static_cast<const char*>(a.v_pool) +
+                      token_at<CT, D>(c, page, head, j0 & ((1 << c.page_shift) - 1)) + (size_t)d * (8 * kEs);
     uint4 w[2 * kEs];
 #pragma unroll
     for (int i = 0; i < 2 * kEs; ++i) w[i] = reinterpret_cast<const uint4*>(src)[i];
@@ -442,12 +509,17 @@ __device__ __forceinline__ void add_nonfinite(const AttendArgs& a, const Geometr
     if (!(bits & kOdd<CT>)) continue;
     float* const out = &y.x;
 #pragma unroll 1
-    for (int key = max(j0, lo); key < min(j0 + 8, hi); ++key)
+    for (int key = max(j0, lo); key < min(j0 + 8, hi); ++key) {
+      if constexpr (TREE) {
+        const int node = key - g.pos0;
+        if (node >= 0 && !(keys.bits[node >> 5] >> (node & 31) & 1u)) continue;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float x = cached<CT>(src + (8 * i + (key & 7)) * kEs);
         if (!(fabsf(x) < INFINITY)) out[i] += x;
       }
+    }
   }
 }
 
@@ -503,7 +575,7 @@ __device__ __forceinline__ void put_record(const Partials& ws, const Start& s, i
 // dealt to many workers) the workgroup takes a row, its groups the parts in turn.
 constexpr int join_groups(int rows) { return rows > 64 ? 16 : 8; }  // workgroups of a segment
 constexpr int kFewParts = 8, kMaxParts = 2 * kCUs;  // (the most workers)
-template <int CT, int D, int ROWS>
+template <int CT, int D, int ROWS, bool TREE>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Split p) {
   constexpr int kLanes = D / 4, kGroups = kAttendThreads / kLanes;  // a float4 a lane
   const Partials ws = partials(a, p);
@@ -511,7 +583,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(AttendArgs a, Sp
   const Record rec = ws.records[worker];
   if (rec.b < 0 || worker != rec.first + 1) return;
   const int parts = rec.last - rec.first + 1;
-  const Geometry g = geometry<ROWS>(a, p, rec.b, rec.row_tile);
+  const Geometry g = geometry<ROWS, TREE>(a, p, rec.b, rec.row_tile);
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const float vs = CT == DSPARK_F8E4M3 ? a.v_scale[rec.head] : 1.f;
   auto slot = [&](int i) __attribute__((always_inline)) { return ws.template slot<D, ROWS>(i == 0 ? rec.slot : 2 * (rec.first + i)); };

@@ -49,7 +49,7 @@ struct KeysTile {
   static constexpr int kS = kF32 ? 1 : 2;  // S^T tiles of 16 keys
   static constexpr int kKeys = 16 * kS;
   static constexpr int kBlocks = D / 16;
-  using V = typename std::conditional<CT == DSPARK_F8E4M3, uint2, uint4>::type;
+  using V = typename std::conditional<is_f8(CT), uint2, uint4>::type;
   // first coordinate of Q register x in lane group g: where K's load has it
   __device__ __forceinline__ static int coord(int x, int g) {
     return kF32 ? 16 * x + 4 * g : CT == DSPARK_BF16 ? 32 * x + 8 * g : 64 * (x >> 1) + 16 * g + 8 * (x & 1);
@@ -80,10 +80,10 @@ __device__ __forceinline__ float groups_sum(float x) {
   return halves32_sum(a.x + a.y);
 }
 
-template <int CT, int D, int NB, int OCC, bool ONCE>
+template <int CT, int D, int NB, int OCC, bool ONCE, bool TREE>
 __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs a, Split p) {
   using TT = KeysTile<CT, D>;
-  constexpr bool kF32 = TT::kF32;
+  constexpr bool kF32 = TT::kF32, kToken = Operand<CT>::kToken;
   constexpr int kRows = NB * 16, kEs = TT::kEs;
   using Data = typename Operand<CT>::Data;
   __shared__ int sh[4];
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
   if (p.workers) {
     // neighbouring workers on one XCD (workgroups go round the 8 of them)
     worker = (blockIdx.x & 7) * (p.workers >> 3) + (blockIdx.x >> 3);
-    s = find_start<kRows, kAttendThreads>(a, p, worker, sh);
+    s = find_start<kRows, kAttendThreads, TREE>(a, p, worker, sh);
     if (s.count == 0) {
       if (threadIdx.x == 0) put_record(partials(a, p), s, worker, 0);
       return;
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
   }
   long long left = s.count;
   bool first_segment = true;
-  Geometry g = geometry<kRows>(a, p, s.b, s.row_tile);
+  Geometry g = geometry<kRows, TREE>(a, p, s.b, s.row_tile);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
   if (g.tiles == 0) return;  // a direct workgroup without rows
 
@@ -133,7 +133,14 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     struct Ids { int a, b; };  // of each 16 keys of the tile
     auto ids_of = [&](int key) __attribute__((always_inline)) { return Ids{row.raw(key), TT::kS == 2 ? row.raw(key + 16) : 0}; };
     auto token = [&](int id, int key) __attribute__((always_inline)) {  // first byte of 16 consecutive tokens
-      return (((size_t)(row.id(id) * (unsigned)c.Hkv + head) << c.page_shift) + (key & off_mask)) * (D * kEs);
+      return token_at<CT, D>(c, row.id(id), head, key & off_mask);
+    };
+    // scales of the lane's 8 keys of the tile, those of its scores and weights
+    auto load_scales = [&](const char* pool, int key0_, Ids id, float4(&s)[2]) __attribute__((always_inline)) {
+      const int key = key0_ + 8 * g16;
+      const char* src = pool + scale_at<D>(c, row.id(g16 < 2 ? id.a : id.b), head, key & off_mask);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[t] = load_key<float4, ONCE>(src + 16 * t);
     };
     auto load_k = [&](int key0_, Ids id, uint4(&k)[TT::kS][TT::kK]) __attribute__((always_inline)) {
       const size_t half[2] = {token(id.a, key0_), token(id.b, key0_ + 16)};
@@ -146,18 +153,20 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
       }
     };
     uint4 k[TT::kS][TT::kK];
+    float4 k_scale[2], v_scale[2];
     Ids id0{}, id1{};
     if (key0 <= last) {
       id0 = ids_of(key0);
       id1 = ids_of(min(key0 + kTurn, last));
       load_k(key0, id0, k);
+      if constexpr (kToken) load_scales(kp, key0, id0, k_scale);
     }
 
     // ---- rows
     const Masks mask{a.causal, a.window, c.len(g.b)};
     const int G = c.Hq / c.Hkv;
     uint4 q[NB][TT::kQ];
-    int row_lo[NB], row_hi[NB];
+    RowKeys<TREE> keys[NB];
     if (threadIdx.x == 0) odd = 0;
     Running run[NB];
     f32x4_t acc[NB][TT::kBlocks];
@@ -168,15 +177,12 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
 #pragma unroll
       for (int db = 0; db < TT::kBlocks; ++db) acc[nb][db] = f32x4_t{};
       const int rho = nb * 16 + col;
-      row_lo[nb] = 0;  // a column without a row sees everything and is left out at the end
-      row_hi[nb] = 0x7fffffff;
+      keys[nb] = {0, 0x7fffffff};  // a column without a row sees everything and is left out at the end
       int hq = 0;
       long long r = -1;
       if (rho < g.rows) {
         r = global_row(a, g, rho, head, hq);
-        const int pos = g.pos0 + (g.row0 + rho) / G;
-        row_lo[nb] = mask.lo(pos);
-        row_hi[nb] = mask.hi(pos);
+        keys[nb] = row_keys<TREE>(a, g, mask, (g.row0 + rho) / G, r);
       }
       const Data* src = static_cast<const Data*>(a.q) + (r >= 0 ? r * a.q_stride + (size_t)hq * D : 0);
 #pragma unroll
@@ -200,6 +206,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
                                : vp + (g16 < 2 ? half[0] : half[1]) + ((g16 & 1) * D + col) * (8 * kEs);
 #pragma unroll
         for (int db = 0; db < TT::kBlocks; ++db) v[db] = load_key<typename TT::V, ONCE>(src + db * (16 * 8 * kEs));
+        if constexpr (kToken) load_scales(vp, key0, id0, v_scale);
       }
       f32x4_t w[NB][TT::kS];
 #pragma unroll
@@ -222,19 +229,39 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
             }
           }
         }
+      if constexpr (kToken) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int t = 0; t < TT::kS; ++t) w[nb][t] *= f32x4_t{k_scale[t].x, k_scale[t].y, k_scale[t].z, k_scale[t].w};
+        load_scales(kp, next, id1, k_scale);
+      }
       load_k(next, id1, k);
       id0 = id1;
       id1 = id2;
       if (key0 < g.all_lo || key0 + TT::kKeys > g.all_hi) {  // not every row sees the whole tile
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const int from = row_lo[nb] - key0 - TT::kGroupKeys * g16;
-          const unsigned n = max(0, row_hi[nb] - row_lo[nb]);
+          if constexpr (TREE) {
+            const uint32_t seen = tree_seen(a, g, keys[nb], key0) >> (TT::kGroupKeys * g16);
+#pragma unroll
+            for (int t = 0; t < TT::kS; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[nb][t][i] = seen >> TT::key_of_reg(t, i) & 1u ? w[nb][t][i] : -INFINITY;
+            continue;
+          }
+          const int from = keys[nb].lo - key0 - TT::kGroupKeys * g16;
+          const unsigned n = max(0, keys[nb].hi - keys[nb].lo);
 #pragma unroll
           for (int t = 0; t < TT::kS; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               w[nb][t][i] = (unsigned)(TT::key_of_reg(t, i) - from) < n ? w[nb][t][i] : -INFINITY;
+        }
+        if constexpr (kToken) {
+#pragma unroll
+          for (int t = 0; t < TT::kS; ++t) v_scale[t] = finite_scales(v_scale[t]);
         }
         uint32_t bits = 0;
 #pragma unroll
@@ -278,7 +305,8 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
           } else {
             bf16x8_t pw, rest;  // the weights in bf16, and what that leaves of them
 #pragma unroll
-            for (int t = 0; t < TT::kS; ++t)
+            for (int t = 0; t < TT::kS; ++t) {
+              if constexpr (kToken) w[nb][t] *= f32x4_t{v_scale[t].x, v_scale[t].y, v_scale[t].z, v_scale[t].w};
 #pragma unroll
               for (int i = 0; i < 4; i += 2) {
                 const f32x2_t x{w[nb][t][i], w[nb][t][i + 1]};
@@ -289,6 +317,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
                 rest[4 * t + i] = z[0];
                 rest[4 * t + i + 1] = z[1];
               }
+            }
 #pragma unroll
             for (int db = 0; db < TT::kBlocks; ++db) {
               const bf16x8_t x = value_operand<CT>(v[db]);
@@ -332,8 +361,11 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
           float4 y = make_float4(o0.x + o1.x + o2.x + o3.x, o0.y + o1.y + o2.y + o3.y, o0.z + o1.z + o2.z + o3.z,
                                  o0.w + o1.w + o2.w + o3.w);
           if (__builtin_expect(odd, 0)) {
-            const int pos = g.pos0 + (g.row0 + rho) / G;
-            add_nonfinite<CT, D, TT::kKeys>(a, g, mask, head, pos, 4 * d4, t0 << 7, t1 << 7, y);
+            int hq;
+            const long long at_row = global_row(a, g, rho, head, hq);
+            if (!TREE || at_row >= 0)
+              add_nonfinite<CT, D, TT::kKeys, TREE>(a, g, row_keys<TREE>(a, g, mask, (g.row0 + rho) / G, at_row), head,
+                                                    4 * d4, t0 << 7, t1 << 7, y);
           }
           if (whole) {
             int hq;
@@ -358,7 +390,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     left -= take;
     if (left <= 0) return;
     first_segment = false;
-    g = next_segment<kRows>(a, p, s);
+    g = next_segment<kRows, TREE>(a, p, s);
   }
 }
 

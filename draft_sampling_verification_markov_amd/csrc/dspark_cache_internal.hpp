@@ -14,9 +14,12 @@ namespace dspark {
 constexpr size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 inline int element_bytes(int dtype) { return dtype == DSPARK_F32 ? 4 : dtype == DSPARK_BF16 ? 2 : 1; }
+constexpr bool is_f8(int dtype) { return dtype == DSPARK_F8E4M3 || dtype == DSPARK_F8E4M3_TOKEN; }
+// bytes of a token's scale, which follow the entries of its page and head
+constexpr int scale_bytes(int dtype) { return dtype == DSPARK_F8E4M3_TOKEN ? 4 : 0; }
 // bytes of one page in one layer of one pool
 inline size_t page_bytes(const dspark_cache& C) {
-  return (size_t)C.Hkv * C.page * C.D * element_bytes(C.cache_dtype);
+  return (size_t)C.Hkv * C.page * (C.D * element_bytes(C.cache_dtype) + scale_bytes(C.cache_dtype));
 }
 inline int log2_page(int page) { return 31 - __builtin_clz((unsigned)page); }
 
@@ -90,8 +93,36 @@ struct AttendArgs {
   float scale2;                 // softmax scale * log2(e)
   int32_t causal, window;
   void* workspace;
+  // a tree's nodes (null otherwise)
+  const uint32_t* mask;  // [n_rows][mask_words]
+  const int32_t* depth;  // [n_rows], or null without a window
+  int32_t mask_words;
 };
 size_t attend_workspace_bytes(const dspark_cache& C, int32_t max_new);
 hipError_t launch_cache_attend(const dspark_cache& C, const AttendArgs& a, hipStream_t s);
+
+// ---- k_attend_tree.hip
+hipError_t launch_tree_attend(const dspark_cache& C, const AttendArgs& a, hipStream_t s);
+
+// ---- k_tree.hip
+struct TreeMaskArgs {
+  const int32_t *parent, *n_new, *row_start;  // n_new, row_start: or null
+  uint32_t* mask;                             // [n_rows][words]
+  int32_t* depth;                             // or null
+  int32_t B, n_rows, max_new, window, words;
+};
+constexpr int kMaxNodes = 1024;
+hipError_t launch_tree_mask(const TreeMaskArgs& a, hipStream_t s);
+
+struct KeepArgs {
+  CacheView c;
+  const int32_t *path, *n_keep;  // [B][max_path], [B]
+  int32_t* length_out;
+  char *k_pool, *v_pool;
+  size_t layer_bytes;
+  int32_t max_path;
+};
+constexpr int kMaxPath = 1024;
+hipError_t launch_tree_keep(const dspark_cache& C, const KeepArgs& a, hipStream_t s);
 
 }  // namespace dspark

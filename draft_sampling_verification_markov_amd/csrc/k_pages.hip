@@ -156,6 +156,101 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int b, int gi)
   }
 }
 
+// The same with a scale for every token and head, taken from the token: the largest size
+// of its D finite elements goes to 448.  A thread quantises 16 elements of a token's key and
+// of its value, whose scale the token's D / 16 threads agree on; the values then change
+// hands through LDS, from a token's elements to a coordinate's tokens.  Old pieces are read
+// only where a group is new in part.
+__device__ __forceinline__ float finite_size(float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; }
+
+template <int THREADS>
+__device__ __forceinline__ float token_scale(const uint32_t (&w)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(finite_size(bf16_lo(w[i])), finite_size(bf16_hi(w[i]))));
+#pragma unroll
+  for (int o = 1; o < THREADS; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  return top > 0.f ? fmaxf(top / 448.f, 0x1p-126f) : 1.f;
+}
+__device__ __forceinline__ uint4 token_entries(const uint32_t (&w)[8], float scale) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = f8_pair(bf16_lo(w[2 * i]) / scale, bf16_hi(w[2 * i]) / scale) |
+           f8_pair(bf16_lo(w[2 * i + 1]) / scale, bf16_hi(w[2 * i + 1]) / scale) << 16;
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_append_token(AppendArgs a, int groups) {
+  constexpr int kPerHead = D / 2, kPieces = D / 16, kHeads = kThreads / kPerHead;
+  __shared__ __attribute__((aligned(16))) uint8_t turn[kHeads][8][D];
+  const CacheView& c = a.c;
+  const int slot = threadIdx.x / kPerHead, at = threadIdx.x % kPerHead;
+  const int head = min((int)blockIdx.y * kHeads + slot, c.Hkv - 1);
+  const bool mine = (int)blockIdx.y * kHeads + slot < c.Hkv;
+  for (long long u = blockIdx.x; u < (long long)c.B * groups; u += gridDim.x) {
+    const int b = (int)(u / groups), gi = (int)(u % groups);
+    const int n = c.rows(b), len = c.len(b);
+    const int pos0 = len - n;  // of token 0; may be negative
+    const int first = pos0 < 0 ? 0 : pos0;
+    const int j0 = ((first >> 3) + gi) << 3;
+    const int lo = j0 > first ? j0 : first, hi = j0 + 8 < len ? j0 + 8 : len;
+    if (n == 0 || lo >= hi) continue;
+    const int page = c.table[(size_t)b * c.max_pages + (j0 >> c.page_shift)];
+    if ((unsigned)page >= (unsigned)c.n_pages) continue;
+    const int off = j0 & ((1 << c.page_shift) - 1);
+    const size_t block = ((size_t)page * c.Hkv + head) << c.page_shift;  // tokens
+    uint8_t* const kb = static_cast<uint8_t*>(a.k_pool) + block * (D + 4);
+    uint8_t* const vb = static_cast<uint8_t*>(a.v_pool) + block * (D + 4);
+    const long long row0 = c.first_row(b) + (j0 - pos0);
+    auto has = [&](int t) { return j0 + t >= lo && j0 + t < hi && c.has_row(row0 + t); };
+    // this thread's 16 elements; a token that is not new reads the nearest row that is there
+    const int t = at / kPieces, piece = at % kPieces;
+    const long long near = row0 + min(max(t, lo - j0), hi - 1 - j0);
+    const long long row = near < 0 ? 0 : near < c.n_rows ? near : (long long)c.n_rows - 1;
+    auto load = [&](const void* x, long long stride, uint32_t(&w)[8]) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + row * stride + head * D) + 2 * piece;
+      const uint4 p = src[0], q = src[1];
+      __builtin_memcpy(w, &p, 16);
+      __builtin_memcpy(w + 4, &q, 16);
+    };
+    uint32_t kw[8], vw[8];
+    load(a.k, a.k_stride, kw);
+    load(a.v, a.v_stride, vw);
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all = all && has(i);
+    uint4 old{};
+    if (!all) old = reinterpret_cast<const uint4*>(vb + (size_t)off * D)[at];
+    const float ks = token_scale<kPieces>(kw), vs = token_scale<kPieces>(vw);
+    const uint4 ke = token_entries(kw, ks), ve = token_entries(vw, vs);
+    if (mine && has(t)) {
+      reinterpret_cast<uint4*>(kb + (size_t)off * D)[at] = ke;
+      if (piece == 0) {
+        const size_t scales = (size_t)D << c.page_shift;
+        reinterpret_cast<float*>(kb + scales)[off + t] = ks;
+        reinterpret_cast<float*>(vb + scales)[off + t] = vs;
+      }
+    }
+    __syncthreads();  // the last group's values are read
+    *reinterpret_cast<uint4*>(&turn[slot][t][16 * piece]) = ve;
+    __syncthreads();
+    uint8_t line[16];
+    __builtin_memcpy(line, &old, 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint16_t x = *reinterpret_cast<const uint16_t*>(&turn[slot][i][2 * at]);
+      const bool is = all || has(i);
+      line[i] = is ? (uint8_t)x : line[i];
+      line[8 + i] = is ? (uint8_t)(x >> 8) : line[8 + i];
+    }
+    uint4 w;
+    __builtin_memcpy(&w, line, 16);
+    if (mine) reinterpret_cast<uint4*>(vb + (size_t)off * D)[at] = w;
+  }
+}
+
 // 8-token groups that a request's new positions can touch
 int append_groups(const dspark_cache& C, const CacheView& v) {
   long long n = v.max_new;
@@ -175,12 +270,19 @@ hipError_t append_typed(const dspark_cache& C, const AppendArgs& a, hipStream_t 
   const int groups = append_groups(C, a.c);
   const long long units = (long long)C.B * groups;
   const dim3 grid(units < 65536 ? (unsigned)units : 65536u, (C.Hkv * (C.D / 2) + kThreads - 1) / kThreads);
+  auto run = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if constexpr (CT == DSPARK_F8E4M3_TOKEN)
+      k_append_token<D><<<grid, kThreads, 0, s>>>(a, groups);
+    else
+      k_append<CT, D><<<grid, kThreads, 0, s>>>(a, groups);
+  };
   if (C.D == 64)
-    k_append<CT, 64><<<grid, kThreads, 0, s>>>(a, groups);
+    run(std::integral_constant<int, 64>());
   else if (C.D == 128)
-    k_append<CT, 128><<<grid, kThreads, 0, s>>>(a, groups);
+    run(std::integral_constant<int, 128>());
   else
-    k_append<CT, 256><<<grid, kThreads, 0, s>>>(a, groups);
+    run(std::integral_constant<int, 256>());
   return hipGetLastError();
 }
 
@@ -706,7 +808,8 @@ hipError_t launch_cache_append(const dspark_cache& C, const AppendArgs& a, hipSt
   switch (C.cache_dtype) {
     case DSPARK_F32: return append_typed<DSPARK_F32>(C, a, s);
     case DSPARK_BF16: return append_typed<DSPARK_BF16>(C, a, s);
-    default: return append_typed<DSPARK_F8E4M3>(C, a, s);
+    case DSPARK_F8E4M3: return append_typed<DSPARK_F8E4M3>(C, a, s);
+    default: return append_typed<DSPARK_F8E4M3_TOKEN>(C, a, s);
   }
 }
 

@@ -1,5 +1,5 @@
-"""ctypes binding of libdspark.so: same entry points as include/dspark.h and
-include/dspark_cache.h.
+"""ctypes binding of libdspark.so: same entry points as include/dspark.h,
+include/dspark_cache.h and include/dspark_tree.h.
 
 This module only marshals arguments: torch tensors supply device pointers and
 torch supplies the current HIP stream.  Every step of the cycle runs in the
@@ -35,9 +35,11 @@ SYMBOLS = ("dspark_workspace_bytes", "dspark_status_string", "dspark_draft", "ds
 # the paged cache (dspark_cache.h)
 CACHE_SYMBOLS = ("dspark_cache_workspace_bytes", "dspark_cache_append", "dspark_cache_attend", "dspark_cache_update",
                  "dspark_cache_compact")
-F8E4M3 = 2  # cache_dtype only
-_CACHE_DT = {"f32": F32, "bf16": BF16, "f8": F8E4M3}
-_CACHE_TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16, F8E4M3: torch.float8_e4m3fn}
+# trees of drafted tokens (dspark_tree.h)
+TREE_SYMBOLS = ("dspark_tree_mask", "dspark_tree_attend", "dspark_tree_keep")
+F8E4M3, F8E4M3_TOKEN = 2, 4  # cache_dtype only
+_CACHE_DT = {"f32": F32, "bf16": BF16, "f8": F8E4M3, "f8t": F8E4M3_TOKEN}
+_CACHE_TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16, F8E4M3: torch.float8_e4m3fn, F8E4M3_TOKEN: torch.uint8}
 
 
 class Problem(ctypes.Structure):
@@ -77,11 +79,24 @@ class Cache(ctypes.Structure):
 
     @property
     def k_shape(self):
+        if self.cache_dtype == F8E4M3_TOKEN:  # entries and scales: token_views
+            return (self.n_layers, self.n_pages, self.Hkv, self.page * (self.D + 4))
         return (self.n_layers, self.n_pages, self.Hkv, self.page, self.D)
 
     @property
     def v_shape(self):
+        if self.cache_dtype == F8E4M3_TOKEN:
+            return self.k_shape
         return (self.n_layers, self.n_pages, self.Hkv, self.page // 8, self.D, 8)
+
+    def token_views(self, pool, values: bool = False):
+        """Entries (float8_e4m3fn, [layers][pages][Hkv][page][D], of values [..][page/8][D][8]) and scales (float32,
+        [layers][pages][Hkv][page]) of a pool with a scale for every token ("f8t"), as views."""
+        if self.cache_dtype != F8E4M3_TOKEN or pool.shape != self.k_shape or pool.dtype != torch.uint8:
+            raise ValueError("not a pool of this cache with a scale for every token")
+        at = self.page * self.D
+        shape = (self.page // 8, self.D, 8) if values else (self.page, self.D)
+        return (pool[..., :at].view(torch.float8_e4m3fn).unflatten(3, shape), pool.view(torch.float32)[..., at // 4:])
 
 
 class DsparkError(RuntimeError):
@@ -162,7 +177,11 @@ def load(debug: bool | None = None) -> ctypes.CDLL:
                                         vp, vp, sz, vp]
     lib.dspark_cache_update.argtypes = [C] + [vp] * 12 + [sz, vp]
     lib.dspark_cache_compact.argtypes = [C] + [vp] * 9 + [sz, vp]
-    for name in CACHE_SYMBOLS[1:]:
+    lib.dspark_tree_mask.argtypes = [i32, vp, i32, vp, vp, i32, i32, vp, vp, vp]
+    lib.dspark_tree_attend.argtypes = [C, i32, vp, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, f, i32, vp, i64,
+                                       vp, vp, sz, vp]
+    lib.dspark_tree_keep.argtypes = [C, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp]
+    for name in CACHE_SYMBOLS[1:] + TREE_SYMBOLS:
         getattr(lib, name).restype = i32
     _libs[debug] = lib
     return lib
@@ -419,15 +438,21 @@ def _count(t, name):
     return t.shape[0]
 
 
-def _device(t):
+def _numel(t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("n_new and row_start must be torch.Tensors")
+    return t.numel()
+
+
+def _device(t, name="k_pool", what="the cache"):
     """The device of the call: that of its tensors, which has to be the current one."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError("k_pool must be a torch.Tensor")
+        raise TypeError(f"{name} must be a torch.Tensor")
     index = t.get_device()
     if index < 0:
-        raise ValueError("the cache's tensors must be device tensors")
+        raise ValueError(f"{what}'s tensors must be device tensors")
     if index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{what} is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
     return index
 
 
@@ -508,6 +533,67 @@ def cache_compact(C: Cache, table, length, ref, table_out, ref_out, n_live, k_po
         _dev(n_live, i32, (1,), dev, "n_live"), _dev(k_pool, ct, C.k_shape, dev, "k_pool"),
         _dev(v_pool, ct, C.v_shape, dev, "v_pool"), ws, nbytes, _stream_of(dev, stream))
     _check("dspark_cache_compact", st)
+
+
+def _words(max_new: int) -> int:
+    """Words of a node's row of a tree's mask."""
+    return (max_new + 31) // 32
+
+
+def tree_mask(parent, n_new, row_start, max_new: int, mask, depth=None, window: int = 0, stream=None) -> None:
+    """Ancestor bits mask [rows][ceil(max_new / 32)] int32 and depths [rows] of the trees whose nodes' parents are
+    parent [rows]; without n_new and row_start each max_new rows are a tree."""
+    lib, dev = load(), _device(parent, "parent", "the tree")
+    i32, rows = torch.int32, (parent.numel(),)
+    given = n_new if n_new is not None else row_start
+    B = (-(-rows[0] // max_new) if max_new > 0 else 0) if given is None else _numel(given)
+    if rows[0] == 0 and given is None:
+        B = 1
+    st = lib.dspark_tree_mask(
+        B, _dev(parent, i32, rows, dev, "parent"), rows[0], _opt(n_new, i32, (B,), dev, "n_new"),
+        _opt(row_start, i32, (B,), dev, "row_start"), max_new, window,
+        _dev(mask, i32, (rows[0], _words(max_new)), dev, "mask"), _opt(depth, i32, rows, dev, "depth"),
+        _stream_of(dev, stream))
+    _check("dspark_tree_mask", st)
+
+
+def tree_attend(C: Cache, layer: int, q, n_new, row_start, max_new: int, mask, depth, length, table, k_pool, v_pool,
+                k_scale, v_scale, out, lse, workspace, scale: float | None = None, window: int = 0, stream=None) -> None:
+    """Attention of the trees' nodes, rows of q [rows][Hq][D], over their context and the nodes of their mask's bits;
+    scale None is D ** -0.5, depth may be None without a window."""
+    lib, dev = load(), _device(k_pool)
+    i32, f32, B, dt, ct = torch.int32, torch.float32, (C.B,), C.data_type, C.cache_type
+    rows = _count(q, "q")
+    qp, qs = _rows(q, dt, (rows, C.Hq, C.D), dev, "q")
+    op, os_ = _rows(out, dt, (rows, C.Hq, C.D), dev, "out")
+    ws, nbytes = _workspace(workspace, dev)
+    st = lib.dspark_tree_attend(
+        C, layer, qp, qs, rows, _opt(n_new, i32, B, dev, "n_new"), _opt(row_start, i32, B, dev, "row_start"),
+        max_new, _dev(mask, i32, (rows, _words(max_new)), dev, "mask"), _opt(depth, i32, (rows,), dev, "depth"),
+        _dev(length, i32, B, dev, "length"), _dev(table, i32, (C.B, C.max_pages), dev, "table"),
+        _dev(k_pool, ct, C.k_shape, dev, "k_pool"), _dev(v_pool, ct, C.v_shape, dev, "v_pool"),
+        _opt(k_scale, f32, (C.Hkv,), dev, "k_scale"), _opt(v_scale, f32, (C.Hkv,), dev, "v_scale"),
+        C.D ** -0.5 if scale is None else scale, window, op, os_, _opt(lse, f32, (rows, C.Hq), dev, "lse"), ws, nbytes,
+        _stream_of(dev, stream))
+    _check("dspark_tree_attend", st)
+
+
+def tree_keep(C: Cache, path, n_keep, n_new, max_new: int, length, table, length_out, k_pool, v_pool, stream=None) -> None:
+    """The keys and values of the new tokens path[b][: n_keep[b]] (ascending) to the places of the first new ones, in all
+    layers; length_out is what the sequences then hold up to them."""
+    lib, dev = load(), _device(k_pool)
+    i32, B, ct = torch.int32, (C.B,), C.cache_type
+    if not isinstance(path, torch.Tensor):
+        raise TypeError("path must be a torch.Tensor")
+    if path.dim() != 2:
+        raise ValueError(f"path has shape {tuple(path.shape)}, expected [{C.B}][nodes]")
+    most = path.shape[1]
+    st = lib.dspark_tree_keep(
+        C, _dev(path, i32, (C.B, most), dev, "path"), _dev(n_keep, i32, B, dev, "n_keep"), most,
+        _opt(n_new, i32, B, dev, "n_new"), max_new, _dev(length, i32, B, dev, "length"),
+        _dev(table, i32, (C.B, C.max_pages), dev, "table"), _dev(length_out, i32, B, dev, "length_out"),
+        _dev(k_pool, ct, C.k_shape, dev, "k_pool"), _dev(v_pool, ct, C.v_shape, dev, "v_pool"), _stream_of(dev, stream))
+    _check("dspark_tree_keep", st)
 
 
 def debug_flags(clear: bool = True) -> int:

@@ -109,7 +109,7 @@ class PagedCache:
 
     table, length and ref are the present sequences; update writes the other set of
     them and swaps the two, compact those of table and ref (so a captured graph holds an even
-    number of updates, and of compactions)."""
+    number of updates, keep's among them, and of compactions)."""
 
     def __init__(self, C: dspark.Cache, max_new: int, device="cuda", k_scale=None, v_scale=None):
         self.C, self.max_new = C, int(max_new)
@@ -128,6 +128,7 @@ class PagedCache:
         self.n_short = torch.zeros(1, dtype=i32, device=device)
         self._none_short = torch.zeros_like(self.n_short)
         self.n_live = torch.zeros(1, dtype=i32, device=device)
+        self._kept = torch.zeros(C.B, dtype=i32, device=device)
         nbytes = dspark.cache_workspace_bytes(C, self.max_new)
         if nbytes == 0:
             raise ValueError("invalid cache")
@@ -159,6 +160,25 @@ class PagedCache:
                stream=None):
         dspark.cache_attend(self.C, layer, q, n_new, row_start, self.max_new, self.length, self.table, self.k, self.v,
                             self.k_scale, self.v_scale, out, lse, self.workspace, scale, causal, window, stream)
+
+    # ---- drafts that form trees (dspark_tree.h); nodes are the new tokens
+    def mask(self, parent, mask, depth=None, n_new=None, row_start=None, window=0, stream=None):
+        """Ancestor bits and depths of the trees with these parents [rows] (dspark_tree_mask)."""
+        if n_new is None and row_start is None and parent.numel() != self.C.B * self.max_new:
+            raise ValueError(f"{parent.numel()} parents for {self.C.B} trees of {self.max_new} nodes")
+        dspark.tree_mask(parent, n_new, row_start, self.max_new, mask, depth, window, stream)
+
+    def tree_attend(self, layer: int, q, mask, out, lse=None, depth=None, n_new=None, row_start=None, scale=None, window=0,
+                    stream=None):
+        dspark.tree_attend(self.C, layer, q, n_new, row_start, self.max_new, mask, depth, self.length, self.table, self.k,
+                           self.v, self.k_scale, self.v_scale, out, lse, self.workspace, scale, window, stream)
+
+    def keep(self, path, n_keep, n_new=None, stream=None):
+        """The accepted nodes path[b][: n_keep[b]] (ascending), and nothing else of the new tokens, stay: their keys and
+        values move to the first new places (dspark_tree_keep), and the sequences end behind them (update)."""
+        dspark.tree_keep(self.C, path, n_keep, n_new, self.max_new, self.length, self.table, self._kept, self.k, self.v,
+                         stream)
+        self.update(self._kept, stream=stream, n_short=self._none_short)
 
 
 def run_cached_cycle(P, x: CycleInputs, o: CycleOutputs, cache: PagedCache, forward, path: int = dspark.DRAFT_AUTO):

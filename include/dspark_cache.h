@@ -30,6 +30,9 @@
  *   v_pool [n_layers][n_pages][Hkv][page/8][D][8]  8 tokens of one coordinate together,
  *     so that the product with the softmax weights reads its operand (8 consecutive
  *     tokens per lane) with one load, and a token's write stays within 8 * D elements.
+ * With a scale for every token (DSPARK_F8E4M3_TOKEN) the page * D bytes of a page's head
+ * are followed by the page's fp32 scales of that head, [page], in both pools: pools of
+ * [n_layers][n_pages][Hkv][page * (D + 4)] bytes.
  * What no sequence holds (other pages, offsets past a length) may contain anything,
  * NaN and infinities included.
  *
@@ -48,7 +51,8 @@
  * max_pages * page <= 2^24; 1 <= n_pages <= 2^24; 1 <= n_layers <= 1024;
  * Hq a multiple of Hkv, 1 <= Hkv, Hq <= 1024; D in {64, 128, 256}; 1 <= max_new <=
  * 2^20, for attend with B * ceil(max_new * Hq / Hkv / 16) <= 2^24.  Types (data = q,
- * k, v, out): fp32 data with an fp32 cache, bf16 data with a bf16 or an e4m3 cache.
+ * k, v, out): fp32 data with an fp32 cache, bf16 data with a bf16 cache or one of e4m3
+ * in either form.
  * Pools, q, k, v, out 16-byte aligned; other arrays 4-byte aligned.
  */
 #ifndef DSPARK_CACHE_H
@@ -61,8 +65,10 @@ extern "C" {
 #endif
 
 /* cache_dtype only: 8-bit floats (4 exponent, 3 mantissa bits, no infinities), with a
- * scale per kv head: value = stored * scale[head]. */
-enum { DSPARK_F8E4M3 = 2 };
+ * scale per kv head that the caller gives, value = stored * scale[head], or with a scale
+ * per token and kv head, of the key and of the value, that dspark_cache_append takes from
+ * the token and keeps in its page. */
+enum { DSPARK_F8E4M3 = 2, DSPARK_F8E4M3_TOKEN = 4 };
 
 typedef struct {
   int32_t B;           /* request slots */
@@ -72,7 +78,7 @@ typedef struct {
   int32_t n_layers;
   int32_t Hq, Hkv, D;  /* query heads, key/value heads, head size; query head i reads kv head i / (Hq / Hkv) */
   int32_t data_dtype;  /* dspark_dtype of q, k, v and out */
-  int32_t cache_dtype; /* dspark_dtype of the pools, or DSPARK_F8E4M3 */
+  int32_t cache_dtype; /* dspark_dtype of the pools, or DSPARK_F8E4M3, DSPARK_F8E4M3_TOKEN */
 } dspark_cache;
 
 /* Bytes of workspace for dspark_cache_attend with up to max_new rows a request,
@@ -89,10 +95,11 @@ size_t dspark_cache_workspace_bytes(const dspark_cache* C, int32_t max_new);
  *          apart, each a multiple of 16 bytes); n_new [B] int32 or NULL (max_new
  *          everywhere); row_start [B] int32 or NULL (b * max_new); length [B];
  *          table [B][max_pages]; k_scale, v_scale [Hkv] fp32, finite and positive,
- *          for an e4m3 cache (ignored otherwise).
+ *          for an e4m3 cache with scales per head (ignored otherwise).
  * In/out:  k_pool, v_pool: layer `layer` receives the tokens; nothing else changes.
  * An e4m3 cache stores x / scale rounded to nearest (ties to even), values past
- * +-448 as +-448, NaN as NaN.  A page that several slots hold must not be written
+ * +-448 as +-448, NaN as NaN.  A token's own scale is max |x| / 448 over the finite of its
+ * D elements (at least 2^-126; 1 where that maximum is 0).  A page that several slots hold must not be written
  * (dspark_cache_update gives every growing slot a private one).  Of 8 neighbouring
  * tokens that are not all new the others' values are read and written back as they
  * are: two calls that append to one page have to be ordered.  n_rows = 0 does
@@ -114,7 +121,7 @@ dspark_status dspark_cache_append(const dspark_cache* C, int32_t layer, const vo
  *
  * Inputs:  q [n_rows][Hq][D] (data_dtype, rows q_stride elements apart, a multiple
  *          of 16 bytes); n_new, row_start, length, table, k_scale, v_scale as above;
- *          scale > 0, scale * log2(e) finite (with an e4m3 cache also times k_scale).
+ *          scale > 0, scale * log2(e) finite (with scales per head also times k_scale).
  * Outputs: out [n_rows][Hq][D] (rows out_stride elements apart); lse
  *          [n_rows][Hq] fp32 or NULL.  Rows that belong to no request are left as
  *          they were.  Outputs must not overlap the inputs or each other.

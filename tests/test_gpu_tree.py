@@ -1,0 +1,378 @@
+"""Drafted trees over the paged cache on the GPU, against the float64 oracle: masks and depths exactly, attention of the
+nodes over all cache types, row counts and windows, the accepted path moved bit for bit, a whole cycle, and graphs."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import tree as ot  # noqa: E402
+from tests import cache_util as cu  # noqa: E402
+from tests import tree_util as tu  # noqa: E402
+from tests.test_gpu_cache import ds  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ mask
+def gpu_mask(ds, parent, n_new, row_start, max_new, window, with_depth=True):  # noqa: F811
+    n_rows = len(parent)
+    mask = torch.full((n_rows, -(-max_new // 32)), -1, dtype=torch.int32, device="cuda")
+    depth = torch.full((n_rows,), -7, dtype=torch.int32, device="cuda") if with_depth else None
+    ds.tree_mask(cu.i32(parent), None if n_new is None else cu.i32(n_new), None if row_start is None else cu.i32(row_start),
+                 max_new, mask, depth, window=window)
+    torch.cuda.synchronize()
+    return mask.cpu().numpy().view(np.uint32), None if depth is None else depth.cpu().numpy()
+
+
+@pytest.mark.parametrize("max_new", [1, 31, 32, 33, 64, 257, 1024])
+@pytest.mark.parametrize("window", [0, 1, 3, 5000])
+def test_mask(ds, max_new, window):  # noqa: F811
+    rng = np.random.default_rng(max_new)
+    n_new = np.array([max_new, 0, max(1, max_new // 3), 1, max_new - 1])
+    row_start = np.cumsum(n_new + 2) - n_new - 1
+    parent = rng.integers(-1, 3, int((n_new + 2).sum()))
+    for k, (n, r) in enumerate(zip(n_new, row_start)):
+        # a random tree, chains, and a star
+        parent[r:r + n] = tu.parents(rng, int(n)) if k in (0, 3) else np.arange(n) - 1 if k == 4 else np.minimum(np.arange(n) - 1, 0)
+    words, depth = ot.mask(parent, n_new, row_start, len(parent), max_new, window)
+    got, d = gpu_mask(ds, parent, n_new, row_start, max_new, window)
+    assert np.array_equal(got, words) and np.array_equal(d, depth)
+    assert np.array_equal(gpu_mask(ds, parent, n_new, row_start, max_new, window, False)[0], words)
+
+
+def test_mask_of_bad_parents_and_rows(ds):  # noqa: F811
+    # parents that come later, lie far outside or are the node itself; rows outside the array; counts outside their range
+    parent = np.array([0, 5, 1, -2 ** 31, 2 ** 31 - 1, 4, 3, 6, 8, 0])
+    n_new, row_start = np.array([6, 99, -3, 4, 2]), np.array([0, 4, 2, 8, -1])
+    for max_new in (6, 40):
+        for b in (0, 1, 3, 4):  # (they share rows: one at a time)
+            w, d = ot.mask(parent, n_new[b:b + 1], row_start[b:b + 1], 10, max_new)
+            got, gd = gpu_mask(ds, parent, n_new[b:b + 1], row_start[b:b + 1], max_new, 0)
+            assert np.array_equal(got, w) and np.array_equal(gd, d)
+
+
+def test_mask_of_equal_trees(ds):  # noqa: F811
+    rng = np.random.default_rng(3)
+    parent = np.concatenate([tu.parents(rng, 20) for _ in range(300)])
+    words, depth = ot.mask(parent, [20] * 300, np.arange(300) * 20, 6000, 20)
+    got, d = gpu_mask(ds, parent, None, None, 20, 0)
+    assert np.array_equal(got, words) and np.array_equal(d, depth)
+
+
+# ------------------------------------------------------------------ attend
+@pytest.mark.parametrize("dtype", tu.TYPES)
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 4), (128, 8, 2), (256, 6, 2), (128, 5, 1)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_attend_ragged(ds, dtype, D, Hq, Hkv, page):  # noqa: F811
+    c = tu.make(1, dtype, page, D, Hq, Hkv, [1, 5, 0, 12, 9, 33], [1, 37, 20, 12, 130, 70], gap=1)
+    _, words, depth = tu.trees(2, c)
+    tu.check(c, *tu.gpu_tree(ds, c, words, None), tu.oracle_tree(c, words, depth))
+
+
+@pytest.mark.parametrize("dtype", tu.TYPES)
+@pytest.mark.parametrize("window", [1, 2, 5, 40, 3000])
+@pytest.mark.parametrize("G", [1, 8])
+def test_attend_windows(ds, dtype, window, G):  # noqa: F811
+    c = tu.make(3, dtype, 32, 128, 2 * G, 2, [9, 1, 17, 0, 40], [100, 260, 17, 40, 333])
+    _, words, depth = tu.trees(4, c, window=window)
+    tu.check(c, *tu.gpu_tree(ds, c, words, depth, window=window), tu.oracle_tree(c, words, depth, window=window))
+
+
+@pytest.mark.parametrize("dtype,D,page", [("bf16", 128, 16), ("bf16", 64, 64), ("f8", 128, 128), ("f32", 64, 32),
+                                          ("bf16", 256, 16), ("f8t", 256, 32), ("f32", 256, 16), ("f8t", 128, 64)])
+@pytest.mark.parametrize("rows,G", [(2, 8), (17, 4), (60, 2), (150, 2), (301, 1)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_row_counts(ds, dtype, D, page, rows, G, wide):  # noqa: F811
+    # every arrangement of rows; with a wide page table the keys are dealt out over the chip and joined
+    c = tu.make(20 + rows, dtype, page, D, 2 * G, 2, [rows, 1, rows // 2], [rows + 333, 700, rows // 2],
+                width=5000 // page if wide else None)
+    _, words, depth = tu.trees(5, c)
+    tu.check(c, *tu.gpu_tree(ds, c, words, depth), tu.oracle_tree(c, words, depth))
+
+
+@pytest.mark.parametrize("base", [0, 1, 15, 16, 31, 32, 33, 63, 64, 95, 96, 127, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_every_context(ds, dtype, base):  # noqa: F811
+    # where the nodes begin among the tiles, the words and the pages
+    c = tu.make(60 + base, dtype, 16, 64, 4, 2, [5, 40, 70], [base + 5, base + 40, base + 70])
+    _, words, depth = tu.trees(6, c)
+    tu.check(c, *tu.gpu_tree(ds, c, words, depth), tu.oracle_tree(c, words, depth))
+
+
+@pytest.mark.parametrize("dtype", tu.TYPES)
+def test_attend_any_bits(ds, dtype):  # noqa: F811
+    # bits that make no tree: none at all, all of them, those of later nodes, a node that does not see itself
+    c = tu.make(7, dtype, 16, 64, 8, 2, [40, 6, 3], [40, 50, 3])
+    rng = np.random.default_rng(8)
+    words = rng.integers(0, 2 ** 32, (len(c.q), 2), dtype=np.uint32)
+    words[[0, 5, 17, 46, 48]] = 0
+    words[[1, 9, 41]] = 0xFFFFFFFF
+    ref = tu.oracle_tree(c, words, np.zeros(len(c.q)))
+    assert np.isneginf(ref[1][[0, 5, 17, 46, 48]]).all()
+    out, lse = tu.gpu_tree(ds, c, words, None)
+    tu.check(c, out, lse, ref)
+    assert (out[[0, 5, 17, 46, 48]] == 0).all()
+
+
+def test_attend_depths_and_counts_out_of_range(ds):  # noqa: F811
+    # depths are clamped to [0, i]; more nodes than the sequence has tokens: the first lie before position 0
+    c = tu.make(9, "bf16", 16, 64, 2, 1, [5, 3, 4], [2, 0, 40])
+    _, words, depth = tu.trees(10, c, window=3)
+    for d in (depth, depth - 100, depth + 100):
+        tu.check(c, *tu.gpu_tree(ds, c, words, d, window=3), tu.oracle_tree(c, words, d, window=3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 40])
+def test_a_chain_gives_what_a_sequence_does(ds, dtype, n):  # noqa: F811
+    # bit for bit: the same kernels and tiles
+    c = tu.make(11, dtype, 16, 128, 8, 2, [n, n - 2], [n + 100, 77])
+    parent = np.concatenate([np.arange(n) - 1, np.arange(n - 2) - 1])
+    words, _ = ot.mask(parent, c.n_new, c.row_start, len(parent), n)
+    out, lse = tu.gpu_tree(ds, c, words, None)
+    want, want_lse = tu.gpu_attend(ds, c)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype", tu.TYPES)
+@pytest.mark.parametrize("rows", [4, 40])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_values_that_are_not_finite(ds, dtype, rows, wide):  # noqa: F811
+    # a node's NaN reaches its descendants and itself only
+    kw = dict(width=200 if wide else None)
+    c = tu.make(12, dtype, 16, 64, 4, 2, [rows, 2], [rows + 50, 30], **kw)
+    parent, words, depth = tu.trees(13, c)
+    clean, _, _, _ = tu.oracle_tree(c, words, depth)
+    node = 1
+    see = np.array([node in chain for chain in ot.ancestors(parent[:rows])])
+    assert see.any() and not see.all()
+    pos = 50 + node
+    p, off = c.table[0, pos // 16], pos % 16
+    for which in ("k", "v"):
+        d = tu.make(12, dtype, 16, 64, 4, 2, [rows, 2], [rows + 50, 30], **kw)
+        if which == "k":
+            d.k_pool[0, p, 0, off, 5] = float("nan")
+        else:
+            d.v_pool[0, p, 0, off // 8, 5, off % 8] = float("nan")
+        out, lse = tu.gpu_tree(ds, d, words, depth)
+        mine = out[:rows]
+        assert torch.isfinite(mine[~see]).all() and torch.isfinite(out[rows:]).all() and torch.isfinite(mine[:, 2:]).all()
+        if which == "k":
+            assert torch.isnan(mine[see][:, :2]).all() and torch.isnan(lse[:rows][see][:, :2]).all()
+        else:
+            assert torch.isnan(mine[see][:, :2, 5]).all() and torch.isfinite(mine[see][:, :2, :5]).all()
+        for r in np.flatnonzero(~see):
+            assert np.allclose(out[r].double().numpy(), clean[r], rtol=2e-2, atol=2e-2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f8t"])
+def test_attend_strides_layers_and_many_requests(ds, dtype):  # noqa: F811
+    i = np.arange(300)
+    c = tu.make(14, dtype, 16, 64, 4, 1, np.where(i % 4 == 3, 0, 1 + i % 6), 6 + (i * 7) % 60, layers=2, poison=False, gap=1)
+    _, words, depth = tu.trees(15, c)
+    C, ws = tu.handle(ds, c, 6, 2)
+    wide = torch.zeros(len(c.q), 6, 64, dtype=torch.bfloat16, device="cuda")
+    q, o = wide[:, 1:5], torch.full((len(c.q), 5, 64), 77.0, dtype=torch.bfloat16, device="cuda")[:, :4]
+    q.copy_(c.q)
+    ds.tree_attend(C, 1, q, cu.i32(c.n_new), cu.i32(c.row_start), 6, tu.words_i32(words), None, cu.i32(c.length),
+                   cu.i32(c.table), *c.pools(), *c.scales(), o, None, ws)
+    tu.check(c, o.cpu(), None, tu.oracle_tree(c, words, depth, layer=1))
+
+
+# ------------------------------------------------------------------ keep
+def places(pool, page, off):
+    return pool[:, page, :, off // 8, :, off % 8] if pool.ndim == 6 else pool[:, page, :, off]
+
+
+def raw(t):
+    """Bits of a pool's entries as integers, in its shape."""
+    return t.contiguous().view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]).numpy()
+
+
+def parts(C, kp, vp, dtype):
+    """The pools' entries (and scales) as integer arrays."""
+    if dtype != "f8t":
+        return [raw(kp.cpu()), raw(vp.cpu())]
+    return [raw(x) for p, values in ((kp, False), (vp, True)) for x in C.token_views(p.cpu(), values)]
+
+
+@pytest.mark.parametrize("dtype", tu.TYPES)
+@pytest.mark.parametrize("D,Hkv,page", [(64, 1, 16), (128, 3, 32), (256, 2, 16)])
+def test_keep(ds, dtype, D, Hkv, page):  # noqa: F811
+    n_new = np.array([1, 20, 0, 40, 33, 7, 12])
+    length = np.array([5, 20, 9, 61, 90, 30, 4])  # (the last: nodes before position 0)
+    c = tu.make(30, dtype, page, D, Hkv, Hkv, n_new, length, layers=2, poison=False)
+    rng = np.random.default_rng(31)
+    most = 21
+    path, n_keep = np.full((7, most), -5), np.array([1, 20, 3, 21, 9, 0, 12])
+    for b, n in enumerate(n_new):
+        m = min(most, n)
+        path[b, :m] = np.sort(rng.choice(n, m, replace=False)) if n else []
+    path[1, :20] = np.arange(20)  # in place already
+    C, _ = tu.handle(ds, c, 40, 2)
+    kp, vp = c.pools()
+    before = parts(C, kp, vp, dtype)
+    out = torch.full((7,), -9, dtype=torch.int32, device="cuda")
+    ds.tree_keep(C, cu.i32(path), cu.i32(n_keep), cu.i32(n_new), 40, cu.i32(length), cu.i32(c.table), out, kp, vp)
+    torch.cuda.synchronize()
+    want_len = ot.keep(before, path, n_keep, n_new, length, c.table, page=page, places=places)
+    assert out.cpu().tolist() == want_len.tolist()
+    for got, want in zip(parts(C, kp, vp, dtype), before):
+        assert np.array_equal(got, want)
+
+
+def test_keep_of_bad_paths(ds):  # noqa: F811
+    # entries outside the nodes are skipped, a page id outside the pool is left alone, counts are clamped
+    n_new, length = np.array([6, 6, 6]), np.array([20, 40, 30])
+    c = tu.make(32, "bf16", 16, 64, 2, 2, n_new, length, poison=False)
+    c.table[2, 1] = 10 ** 7
+    path = np.array([[2, 99, 5, -1], [1, 3, 2 ** 31 - 1, 5], [1, 2, 3, 4]])
+    n_keep = np.array([99, 4, 2])
+    C, _ = tu.handle(ds, c, 6)
+    kp, vp = c.pools()
+    before = parts(C, kp, vp, "bf16")
+    out = torch.empty(3, dtype=torch.int32, device="cuda")
+    ds.tree_keep(C, cu.i32(path), cu.i32(n_keep), cu.i32(n_new), 6, cu.i32(length), cu.i32(c.table), out, kp, vp)
+    ot.keep(before, path[:2], n_keep[:2], n_new[:2], length[:2], c.table[:2], page=16, places=places)
+    assert out.cpu().tolist() == [18, 38, 26]
+    for got, want in zip(parts(C, kp, vp, "bf16"), before):
+        assert np.array_equal(got, want)
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("dtype", tu.TYPES)
+def test_a_cycle_of_trees(ds, dtype):  # noqa: F811
+    """Trees appended, judged and cut to an accepted path, twice; then the sequences hold what the accepted tokens alone
+    would have left, and a token's attention over them is the same."""
+    from draft_sampling_verification_markov_amd.runner import PagedCache
+    B, T, L, Hq, Hkv, D = 3, 12, 2, 4, 2, 64
+    data = cu.DATA["f8" if dtype == "f8t" else dtype]
+    C = ds.Cache.make(B, 40, 16, 8, L, Hq, Hkv, D, q="f32" if dtype == "f32" else "bf16", cache=dtype)
+    tree, plain = PagedCache(C, T), PagedCache(C, T)
+    rng, gen = np.random.default_rng(70), torch.Generator(device="cuda").manual_seed(70)
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=gen).to(data)  # noqa: E731
+    for turn in range(3):
+        n = rng.integers(1, T + 1, B)
+        parent = np.concatenate([np.pad(tu.parents(rng, int(x)), (0, T - x), constant_values=-1) for x in n])
+        n_new, start = cu.i32(n), cu.i32(np.arange(B) * T)
+        mask, depth = (torch.empty(B * T, 1, dtype=torch.int32, device="cuda"), torch.empty(B * T, dtype=torch.int32, device="cuda"))
+        path, m = np.full((B, 6), -1), []
+        for b in range(B):
+            chain = ot.ancestors(parent[b * T:b * T + n[b]])[int(rng.integers(0, n[b]))][::-1][:6]
+            path[b, :len(chain)] = chain
+            m.append(len(chain))
+        length0 = tree.length.clone()
+        tree.update(tree.length + n_new)
+        tree.mask(cu.i32(parent), mask, depth, n_new, start)
+        kv = [(rnd(B * T, Hkv, D), rnd(B * T, Hkv, D)) for _ in range(L)]
+        q = rnd(B * T, Hq, D)
+        outs = []
+        for layer in range(L):
+            tree.append(layer, *kv[layer], n_new=n_new, row_start=start)
+            out = torch.zeros_like(q)
+            tree.tree_attend(layer, q, mask, out, depth=depth, n_new=n_new, row_start=start)
+            outs.append(out)
+        tree.keep(cu.i32(path), cu.i32(m), n_new=n_new)
+        assert torch.equal(tree.length, length0 + cu.i32(m))
+        # the accepted tokens alone, as a sequence
+        take = torch.tensor(np.concatenate([b * T + path[b, :m[b]] for b in range(B)]), device="cuda")
+        plain.update(plain.length + cu.i32(m))
+        s1 = cu.i32(np.cumsum(m) - m)
+        for layer in range(L):
+            plain.append(layer, kv[layer][0][take], kv[layer][1][take], n_new=cu.i32(m), row_start=s1)
+            out = torch.zeros_like(q[take])
+            plain.attend(layer, q[take], out, n_new=cu.i32(m), row_start=s1)
+            # another order of the same sums: a few roundings of fp32, and one of the type
+            tol = 4e-6 if dtype == "f32" else 2 ** -7
+            assert torch.allclose(outs[layer][take].float(), out.float(), rtol=tol, atol=tol), (turn, layer)
+    n_new = cu.i32([1] * B)
+    for x in (tree, plain):
+        x.update(x.length + 1)
+    q, k, v = rnd(B, Hq, D), rnd(B, Hkv, D), rnd(B, Hkv, D)
+    got = []
+    for x in (tree, plain):
+        out = torch.zeros_like(q)
+        for layer in range(L):
+            x.append(layer, k, v, n_new=n_new, row_start=cu.i32(np.arange(B)))
+            x.attend(layer, q, out, n_new=n_new, row_start=cu.i32(np.arange(B)))
+        got.append(out)
+    assert torch.equal(tree.length, plain.length) and torch.equal(*got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f8t"])
+def test_graph_of_a_tree(ds, dtype):  # noqa: F811
+    """Mask, append, attend and keep captured once and replayed with other trees, each replay against the eager calls;
+    two graphs that share a workspace, in turn."""
+    B, T, Hq, Hkv, D, page = 2, 20, 8, 2, 128, 16
+    c = tu.make(80, dtype, page, D, Hq, Hkv, [T, T], [T + 40, T + 9], poison=False)
+    C, ws = tu.handle(ds, c, T)
+    first = c.pools()
+    kp, vp = (x.clone() for x in first)
+    n_new, start, length, table = cu.i32(c.n_new), cu.i32(c.row_start), cu.i32(c.length), cu.i32(c.table)
+    parent, path, n_keep = cu.i32(np.full(2 * T, -1)), cu.i32(np.full((2, 4), -1)), cu.i32([0, 0])
+    k, v, q = (torch.zeros(2 * T, h, D, dtype=torch.bfloat16, device="cuda") for h in (Hkv, Hkv, Hq))
+    mask, depth = torch.zeros(2 * T, 1, dtype=torch.int32, device="cuda"), torch.zeros(2 * T, dtype=torch.int32, device="cuda")
+    out, lse, cut = torch.zeros_like(q), torch.zeros(2 * T, Hq, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    sc = c.scales()
+
+    def judge():
+        ds.tree_mask(parent, n_new, start, T, mask, depth, window=6)
+        ds.cache_append(C, 0, k, v, n_new, start, T, length, table, *sc, kp, vp)
+        ds.tree_attend(C, 0, q, n_new, start, T, mask, depth, length, table, kp, vp, *sc, out, lse, ws, window=6)
+
+    def cut_to():
+        ds.tree_keep(C, path, n_keep, n_new, T, length, table, cut, kp, vp)
+        ds.cache_attend(C, 0, q, n_new, start, T, length, table, kp, vp, *sc, out, None, ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        judge()
+        cut_to()
+    side.synchronize()
+    graphs = []
+    for f in (judge, cut_to):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        graphs.append(g)
+    rng, gen = np.random.default_rng(81), torch.Generator(device="cuda").manual_seed(81)
+    for turn in range(4):
+        tree = np.concatenate([tu.parents(rng, T) for _ in range(2)])
+        parent.copy_(cu.i32(tree))
+        chain = [ot.ancestors(tree[b * T:(b + 1) * T])[int(rng.integers(5, T))][::-1][:4] for b in range(2)]
+        path.copy_(cu.i32([x + [-1] * (4 - len(x)) for x in chain]))
+        n_keep.copy_(cu.i32([len(x) for x in chain]))
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, device="cuda", generator=gen))
+        results = []
+        for mode in ("eager", "graph"):
+            kp.copy_(first[0])
+            vp.copy_(first[1])
+            for x in (mask, depth, out, lse, cut):
+                x.zero_()
+            got = []
+            for f, g in zip((judge, cut_to), graphs):
+                f() if mode == "eager" else g.replay()
+                torch.cuda.synchronize()
+                got += [x.clone() for x in (mask, depth, out, lse, cut, kp.view(torch.uint8), vp.view(torch.uint8))]
+            results.append(got)
+        for a, b in zip(*results):
+            assert torch.equal(a, b), turn
+        words, d = ot.mask(tree, c.n_new, c.row_start, 2 * T, T, 6)
+        assert np.array_equal(results[1][0].cpu().numpy().view(np.uint32), words)
+
+
+def test_another_stream(ds):  # noqa: F811
+    c = tu.make(90, "bf16", 16, 64, 4, 2, [30, 9], [200, 100])
+    _, words, depth = tu.trees(91, c)
+    C, ws = tu.handle(ds, c, 30)
+    q, out = c.q.cuda(), torch.zeros_like(c.q, device="cuda")
+    n, rs, m, le, ta = cu.i32(c.n_new), cu.i32(c.row_start), tu.words_i32(words), cu.i32(c.length), cu.i32(c.table)
+    kp, vp = c.pools()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ds.tree_attend(C, 0, q, n, rs, 30, m, None, le, ta, kp, vp, None, None, out, None, ws, stream=side)
+    side.synchronize()
+    tu.check(c, out.cpu(), None, tu.oracle_tree(c, words, depth))
