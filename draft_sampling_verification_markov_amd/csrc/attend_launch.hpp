@@ -3,7 +3,7 @@
 #pragma once
 
 #include "attend_keys.hpp"
-#include "attend_rows.hpp"
+#include "attend_parts.hpp"
 
 namespace dspark {
 namespace {
@@ -29,6 +29,11 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows
 // over 1000 52.0 / 53.4), and one prompt of 2048 rows among 255 tokens has the row tiles of
 // all of them launched (1957 us; in calls of their own 121 + 391).
+// Trees differ in their size, so that most of the row tiles that the largest needs are empty
+// in the others: a pair's row tiles count as two at most (8 requests of up to 256 nodes, 16
+// row tiles x 4 heads, over up to 32768 keys 1010 us whole, 252 dealt; 8 of 256, 8 x 8, over
+// 8192 151 / 85; 32 of 64, 2 x 4, over 4000 162 / 102; but 64 of 64, 2 x 8, over 4096 142 /
+// 182; 128 of 64 258 / 363).
 // Dealt ones go to one worker a CU, or to two where there are enough keys (`twice`): the
 // second hides the other's waits, but doubles the partial results and halves their shares.
 constexpr int kFewKeys = 1024, kSomeKeys = 4096;
@@ -42,14 +47,15 @@ long long most_keys(const dspark_cache& C, int32_t max_new, int window) {
   const long long row = (long long)C.max_pages * C.page, seen = (long long)window + max_new;
   return window > 0 && seen < row ? seen : row;
 }
+template <bool TREE>
 Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int unit_shift, int per_cu, const Rule& r) {
   Split pl{};
   pl.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
   pl.unit_shift = unit_shift;
   const long long keys = most_keys(C, max_new, window);
-  const long long segments = (long long)C.B * pl.row_tiles * C.Hkv;
-  const bool direct = segments <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
-                                                (pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
+  const long long pairs = (long long)C.B * C.Hkv, segments = pairs * (TREE && pl.row_tiles > 2 ? 2 : pl.row_tiles);
+  const bool direct = pairs * pl.row_tiles <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
+                                                (!TREE && pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
   pl.longest_first = C.B > 1 && C.B <= kAttendThreads && segments > 2 * kCUs && keys > kFewKeys && window == 0;
   pl.workers = direct ? 0 : per_cu > 1 && segments * keys >= r.twice ? 2 * kCUs : kCUs;
   return pl;
@@ -93,7 +99,7 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   constexpr int kHeld = (OCC > 2 ? OCC : 2) * kCUs;
   const Rule rule{CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys, C.B <= kAttendThreads ? kHeld : 16 * kHeld,
                   NB == 1 ? 1 << 22 : 1 << 20};
-  const Split pl = plan_for(C, a.c.max_new, a.window, NB * 16, 7, OCC, rule);
+  const Split pl = plan_for<TREE>(C, a.c.max_new, a.window, NB * 16, 7, OCC, rule);
   const bool once = read_once(C, pl, a.c.max_new, a.window);
   return run_plan<CT, D, NB * 16, TREE>(
       C, a, pl, once ? k_attend_keys<CT, D, NB, OCC, NB == 1, TREE> : k_attend_keys<CT, D, NB, OCC, false, TREE>, s);
@@ -105,10 +111,13 @@ hipError_t run_rows(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   // `twice`: 12 segments of 17123 keys 42 us with one worker a CU, 50 with two; 20 of 132768
   // 159 / 115
   constexpr Rule kRule{kFewKeys, 2 * kCUs, 1 << 20};
-  const Split pl = plan_for(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, 2, kRule);
+  const Split pl = plan_for<TREE>(C, a.c.max_new, a.window, S::kRows, S::kKeys == 64 ? 6 : 5, 2, kRule);
   const bool once = read_once(C, pl, a.c.max_new, a.window);
-  return run_plan<CT, D, S::kRows, TREE>(C, a, pl, once ? k_attend_rows<CT, D, true, TREE> : k_attend_rows<CT, D, false, TREE>,
-                                         s);
+  if constexpr (TREE || Operand<CT>::kToken)
+    return run_plan<CT, D, S::kRows, TREE>(
+        C, a, pl, once ? k_attend_parts<CT, D, true, TREE> : k_attend_parts<CT, D, false, TREE>, s);
+  else
+    return run_plan<CT, D, S::kRows, TREE>(C, a, pl, once ? k_attend_rows<CT, D, true> : k_attend_rows<CT, D, false>, s);
 }
 
 // Workgroups of k_attend_keys that a CU holds, by their registers.

@@ -62,13 +62,6 @@ __device__ __forceinline__ void mask_scores(f32x16_t& s, int lo, int hi, int h) 
   for (int i = 0; i < 16; ++i) s[i] = (unsigned)(key_of_reg(i) - from) < n ? s[i] : -INFINITY;
 }
 
-// The same from a bit for each of the tile's 32 keys.
-__device__ __forceinline__ void mask_scores(f32x16_t& s, uint32_t seen, int h) {
-  seen >>= 8 * h;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = seen >> key_of_reg(i) & 1u ? s[i] : -INFINITY;
-}
-
 // The running maximum over N score tiles of a row; returns the factor by which O and l
 // fade (1 for most tiles).
 template <int N>
@@ -122,7 +115,6 @@ struct RowsShape {
   static constexpr int kBytes = kKeys * D * kEs;             // of the keys (or the values) of a tile
   static constexpr int kPieces = D * kEs / 16;               // of a key
   static constexpr int kOps = kBytes / 1024 / 4;               // DMA instructions a wave, keys (or values)
-  static constexpr int kGroup = kOps + Operand<CT>::kToken;    // and their scales
   static constexpr int kAhead = D == 256 ? 3 : 4;            // LDS reads before their products (more spill at 256)
   static constexpr int kQ = D / 16;                          // registers of Q (16 bytes a lane)
   static constexpr int kBlocks = D / 32;                     // of 32 coordinates
@@ -146,24 +138,14 @@ __device__ __forceinline__ void dma_1k(__amdgpu_buffer_rsrc_t src, int offset, u
                                            ONCE ? 2 : 0);
 }
 
-// 64 lanes x 4 bytes, in lane order; past the buffer's end zeros
-template <bool ONCE>
-__device__ __forceinline__ void dma_words(__amdgpu_buffer_rsrc_t src, int offset, float* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 4, offset, 0, 0, ONCE ? 2 : 0);
-}
-
 // ONCE: keys and values with the streaming policy
-template <int CT, int D, bool ONCE, bool TREE>
+template <int CT, int D, bool ONCE>
 __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_rows(AttendArgs a, Split p) {
   using S = RowsShape<CT, D>;
   constexpr int kQ = S::kQ, kRows = S::kRows, kEs = S::kEs;
   constexpr int kOps = S::kOps;
   constexpr int kWavesPerSub16 = 4 / (S::kKeys / 16);  // waves that share the DMA of 16 keys
   __shared__ __attribute__((aligned(1024))) unsigned char k0[S::kBytes], k1[S::kBytes], v0[S::kBytes], v1[S::kBytes];
-  // scales of a token: each wave brings those of its 16 keys into 64 words of its own
-  constexpr bool kToken = Operand<CT>::kToken;
-  constexpr int kScales = kToken ? kAttendThreads : 1;
-  __shared__ __attribute__((aligned(256))) float ks0[kScales], ks1[kScales], vs0[kScales], vs1[kScales];
   __shared__ int sh[4];
   __shared__ int odd;  // a value that is not finite, and that a row sees, was replaced
   const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
@@ -174,7 +156,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
   int worker = 0;
   if (p.workers) {
     worker = (blockIdx.x & 7) * (p.workers >> 3) + (blockIdx.x >> 3);
-    s = find_start<kRows, kAttendThreads, TREE>(a, p, worker, sh);
+    s = find_start<kRows, kAttendThreads, false>(a, p, worker, sh);
     if (s.count == 0) {
       if (threadIdx.x == 0) put_record(partials(a, p), s, worker, 0);
       return;
@@ -185,7 +167,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
   }
   long long left = s.count;
   bool first_segment = true;
-  Geometry g = geometry<kRows, TREE>(a, p, s.b, s.row_tile);
+  Geometry g = geometry<kRows, false>(a, p, s.b, s.row_tile);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
   if (g.tiles == 0) return;
 
@@ -217,13 +199,13 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     int some_lo = 0, some_hi = 0, all_lo = 0, all_hi = 0;
     if (wrows > 0) {
       const int first = g.pos0 + (g.row0 + wrow) / G, last = g.pos0 + (g.row0 + wrow + wrows - 1) / G;
-      some_lo = mask.lo(TREE ? g.pos0 : first);
+      some_lo = mask.lo(first);
       some_hi = mask.hi(last);
       all_lo = mask.lo(last);
-      all_hi = TREE ? g.all_hi : mask.hi(first);
+      all_hi = mask.hi(first);
     }
     uint4 q[kQ];
-    RowKeys<TREE> keys{0, 0x7fffffff};  // a column without a row sees everything and is left out at the end
+    int row_lo = 0, row_hi = 0x7fffffff;  // a column without a row sees everything and is left out at the end
     Running run{-INFINITY, 0.f};
     f32x16_t acc[S::kBlocks];
     const int rho = wrow + col;
@@ -234,7 +216,9 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       long long r = -1;
       if (rho < g.rows) {
         r = global_row(a, g, rho, head, hq);
-        keys = row_keys<TREE>(a, g, mask, (g.row0 + rho) / G, r);
+        const int pos = g.pos0 + (g.row0 + rho) / G;
+        row_lo = mask.lo(pos);
+        row_hi = mask.hi(pos);
       }
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (r >= 0 ? r * a.q_stride + (size_t)hq * D : 0);
 #pragma unroll
@@ -249,23 +233,16 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     // the 16 keys (or values) of tile t that this wave brings, as a buffer
     auto source = [&](const void* pool, int raw, int t) __attribute__((always_inline)) {
       const int key = min(t, t1 - 1) * S::kKeys + 16 * sub16;
-      const size_t at = token_at<CT, D>(c, row.id(raw), head, key & ((1 << c.page_shift) - 1));
-      return make_rsrc(static_cast<const char*>(pool) + at, 16 * D * kEs);
+      const size_t token = ((size_t)(row.id(raw) * (unsigned)c.Hkv + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+      return make_rsrc(static_cast<const char*>(pool) + token * (D * kEs), 16 * D * kEs);
     };
-    auto dma_scales = [&](const void* pool, int raw, int t, float* to) __attribute__((always_inline)) {
-      const int key = min(t, t1 - 1) * S::kKeys + 16 * sub16;
-      const size_t at = scale_at<D>(c, row.id(raw), head, key & ((1 << c.page_shift) - 1));
-      dma_words<ONCE>(make_rsrc(static_cast<const char*>(pool) + at, 16 * 4), 4 * lane, to + 64 * wave);
-    };
-    auto dma_k = [&](int raw, int t, unsigned char* to, float* scales) __attribute__((always_inline)) {
+    auto dma_k = [&](int raw, int t, unsigned char* to) __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t src = source(a.k_pool, raw, t);
 #pragma unroll
       for (int i = 0; i < kOps; ++i) dma_1k<0, ONCE>(src, k_src[i], to + (wave * kOps + i) * 1024);
-      if constexpr (kToken) dma_scales(a.k_pool, raw, t, scales);
     };
-    auto dma_v = [&](int raw, int t, unsigned char* to, float* scales) __attribute__((always_inline)) {
+    auto dma_v = [&](int raw, int t, unsigned char* to) __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t src = source(a.v_pool, raw, t);
-      if constexpr (kToken) dma_scales(a.v_pool, raw, t, scales);
       unsigned char* const at = to + wave * kOps * 1024;
       dma_1k<0, ONCE>(src, v_src, at);
       if constexpr (kOps > 1) dma_1k<1024, ONCE>(src, v_src, at);
@@ -293,38 +270,17 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       return value_operand<CT>(
           *reinterpret_cast<const typename S::V*>(vb + ((sub * 4 + 2 * sl + h) * D + 32 * db + col) * (8 * kEs)));
     };
-    // the scales of the keys of score registers 8 j .. 8 j + 7 of half tile `sub`
-    auto scales_of = [&](const float* sc, int sub, int j, float4(&s)[2]) __attribute__((always_inline)) {
-      const float4* src = reinterpret_cast<const float4*>(sc + (2 * sub + j) * kWavesPerSub16 * 64 + 8 * h);
-      s[0] = src[0];
-      s[1] = src[1];
-    };
-    auto times_scales = [&](const float* sc, int sub, f32x16_t& w) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float4 s[2];
-        scales_of(sc, sub, j, s);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          w[8 * j + 4 * i] *= s[i].x;
-          w[8 * j + 4 * i + 1] *= s[i].y;
-          w[8 * j + 4 * i + 2] *= s[i].z;
-          w[8 * j + 4 * i + 3] *= s[i].w;
-        }
-      }
-    };
     // Waits until at most the youngest two of this wave's DMA groups (of keys or of values)
     // are on their way.  Past the last tile the last one is brought again, so that there
     // are always as many and the compiler, which counts too, adds no waits of its own.
-    auto landed = [&]() __attribute__((always_inline)) { wait_vmem_n<2 * S::kGroup>(); };
+    auto landed = [&]() __attribute__((always_inline)) { wait_vmem_n<2 * kOps>(); };
     // One tile, keys in kb and values in vb; v_next receives the next tile's values and kb,
     // once read, the keys of the one after.  Every group of DMA is sent one and a half
-    // tiles before it is used.  Scales of a token go with their entries: kc with kb, ...
-    auto step = [&](int t, int id1, int id2, unsigned char* kb, unsigned char* vb, unsigned char* v_next, float* kc,
-                    float* vc, float* vc_next) __attribute__((always_inline)) {
+    // tiles before it is used.
+    auto step = [&](int t, int id1, int id2, unsigned char* kb, unsigned char* vb, unsigned char* v_next) __attribute__((always_inline)) {
       landed();            // this wave's part of the keys
       barrier_lds_only();  // everybody's, and the last tile's values are read
-      dma_v(id1, t + 1, v_next, vc_next);
+      dma_v(id1, t + 1, v_next);
       const int key0 = t * S::kKeys;
       const bool on = key0 < some_hi && key0 + S::kKeys > some_lo;  // something that this wave's rows see
       f32x16_t w[S::kSubs];
@@ -340,18 +296,10 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
           schedule<kLdsRead, 1>();
         }
         schedule<kMfma, S::kAhead * kMma>();
-        if constexpr (kToken) {
-#pragma unroll
-          for (int sub = 0; sub < S::kSubs; ++sub) times_scales(kc, sub, w[sub]);
-        }
         if (key0 < all_lo || key0 + S::kKeys > all_hi) {
 #pragma unroll
-          for (int sub = 0; sub < S::kSubs; ++sub) {
-            if constexpr (TREE)
-              mask_scores(w[sub], tree_seen(a, g, keys, key0 + 32 * sub), h);
-            else
-              mask_scores(w[sub], keys.lo - (key0 + 32 * sub), keys.hi - (key0 + 32 * sub), h);
-          }
+          for (int sub = 0; sub < S::kSubs; ++sub)
+            mask_scores(w[sub], row_lo - (key0 + 32 * sub), row_hi - (key0 + 32 * sub), h);
         }
         const float fade = raise_max(w, run, ks);
         if (__any(fade != 1.f)) {
@@ -361,10 +309,9 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
       }
       landed();            // this wave's part of the values
       barrier_lds_only();  // everybody's, and the keys are read
-      dma_k(id2, t + 2, kb, kc);
+      dma_k(id2, t + 2, kb);
       if (key0 < g.all_lo || key0 + S::kKeys > g.all_hi) {
         // a tile that not all rows see whole: its values are made finite, in place
-        if constexpr (kToken) vc[threadIdx.x] = finite_scale(vc[threadIdx.x]);
         uint4* const mine = reinterpret_cast<uint4*>(vb) + threadIdx.x;
         uint32_t bits = 0;
 #pragma unroll
@@ -389,7 +336,6 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
 #pragma unroll
       for (int sub = 0; sub < S::kSubs; ++sub) {
         weights(w[sub], run, ks);
-        if constexpr (kToken) times_scales(vc, sub, w[sub]);
 #pragma unroll
         for (int sl = 0; sl < 2; ++sl) {
           const bf16x8_t pw = pack8(w[sub], 8 * sl);
@@ -414,14 +360,14 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     int id0 = raw_id(t0), id1 = raw_id(t0 + 1), id2 = raw_id(t0 + 2);
     barrier_lds_only();  // the last segment's tiles are read
     if (threadIdx.x == 0) odd = 0;
-    dma_k(id0, t0, k0, ks0);
-    dma_v(id0, t0, v0, vs0);
-    dma_k(id1, t0 + 1, k1, ks1);
+    dma_k(id0, t0, k0);
+    dma_v(id0, t0, v0);
+    dma_k(id1, t0 + 1, k1);
     for (int t = t0; t < t1; t += 2) {
       const int id3 = raw_id(t + 3), id4 = raw_id(t + 4);
-      step(t, id1, id2, k0, v0, v1, ks0, vs0, vs1);
+      step(t, id1, id2, k0, v0, v1);
       if (t + 1 == t1) break;
-      step(t + 1, id2, id3, k1, v1, v0, ks1, vs1, vs0);
+      step(t + 1, id2, id3, k1, v1, v0);
       id1 = id3;
       id2 = id4;
     }
@@ -453,11 +399,11 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
             store4<CT>(a.out, r * a.out_stride + (size_t)hq * D + d, y);
         }
       if (__builtin_expect(any_odd && !none, 0)) {
-        const RowKeys<TREE> sees = row_keys<TREE>(a, g, mask, (g.row0 + rho) / G, r);
+        const RowKeys<false> sees = row_keys<false>(a, g, mask, (g.row0 + rho) / G, r);
 #pragma unroll 1
         for (int d = 4 * h; d < D; d += 8) {
           float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!TREE || r >= 0) add_nonfinite<CT, D, S::kKeys, TREE>(a, g, sees, head, d, t0 * S::kKeys, t1 * S::kKeys, y);
+          add_nonfinite<CT, D, S::kKeys, false>(a, g, sees, head, d, t0 * S::kKeys, t1 * S::kKeys, y);
           const size_t at = whole ? r * a.out_stride + (size_t)hq * D + d : 0;
           float4* const part = reinterpret_cast<float4*>(slot + (size_t)rho * D + d);
           if (whole && r < 0) continue;
@@ -481,7 +427,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
     left -= take;
     if (left <= 0) return;
     first_segment = false;
-    g = next_segment<kRows, TREE>(a, p, s);
+    g = next_segment<kRows, false>(a, p, s);
   }
 }
 

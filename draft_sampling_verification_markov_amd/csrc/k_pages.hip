@@ -158,26 +158,66 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int b, int gi)
 
 // The same with a scale for every token and head, taken from the token: the largest size
 // of its D finite elements goes to 448.  A thread quantises 16 elements of a token's key and
-// of its value, whose scale the token's D / 16 threads agree on; the values then change
-// hands through LDS, from a token's elements to a coordinate's tokens.  Old pieces are read
-// only where a group is new in part.
-__device__ __forceinline__ float finite_size(float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; }
+// of its value; the token's D / 16 threads, neighbours in a row of 16 lanes, agree on the
+// scale.  The values then change hands through LDS, from a token's elements to a coordinate's
+// tokens.  Old pieces are read only where a group is new in part.
+constexpr uint32_t kInf16 = 0x7F80;  // bf16
 
-template <int THREADS>
-__device__ __forceinline__ float token_scale(const uint32_t (&w)[8]) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(finite_size(bf16_lo(w[i])), finite_size(bf16_hi(w[i]))));
-#pragma unroll
-  for (int o = 1; o < THREADS; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-  return top > 0.f ? fmaxf(top / 448.f, 0x1p-126f) : 1.f;
+// The larger of x and another lane's, by a data-parallel primitive.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t x) {
+  const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+  return x > y ? x : y;
 }
-__device__ __forceinline__ uint4 token_entries(const uint32_t (&w)[8], float scale) {
-  uint32_t o[4];
+// Largest size of the elements of a token's THREADS threads, as bf16 bits: sizes of bf16
+// numbers are ordered as their bits are.  odd: an element is not finite (and left out).
+template <int THREADS>
+__device__ __forceinline__ uint32_t token_top(const uint32_t (&w)[8], bool& odd) {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  u16x2_t top = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = f8_pair(bf16_lo(w[2 * i]) / scale, bf16_hi(w[2 * i]) / scale) |
-           f8_pair(bf16_lo(w[2 * i + 1]) / scale, bf16_hi(w[2 * i + 1]) / scale) << 16;
+  for (int i = 0; i < 8; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu));
+  uint32_t t = top[0] > top[1] ? top[0] : top[1];
+  odd = t >= kInf16;
+  if (__builtin_expect(odd, 0)) {
+    t = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = w[i >> 1] >> (16 * (i & 1)) & 0x7FFFu;
+      if (x < kInf16 && x > t) t = x;
+    }
+  }
+  t = max_with<0xB1>(t);   // lanes 1, 0, 3, 2
+  t = max_with<0x4E>(t);   // lanes 2, 3, 0, 1
+  if constexpr (THREADS > 4) t = max_with<0x141>(t);  // lanes 7 .. 0 of each 8
+  if constexpr (THREADS > 8) t = max_with<0x140>(t);  // lanes 15 .. 0 of each 16
+  return t;
+}
+__device__ __forceinline__ float token_scale(uint32_t top) {
+  return top ? fmaxf(__uint_as_float(top << 16) / 448.f, 0x1p-126f) : 1.f;
+}
+// e4m3 of the 16 quotients x / scale.  With r the rounded reciprocal of the scale and q = x r,
+// the rest x - q scale is exact in an fma, and q plus the rest times r is the rounded quotient
+// (Markstein, 1990): three instructions where a division takes ten.  Scales so small that the
+// rest could fall among the subnormal numbers, and elements that are not finite, are divided.
+// (No quotient of a finite element lies above 448 by more than a rounding, which goes to 448.)
+__device__ __forceinline__ uint4 token_entries(const uint32_t (&w)[8], float scale, bool odd) {
+  uint32_t o[4] = {0, 0, 0, 0};
+  if (__builtin_expect(odd || scale < 0x1p-90f, 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i >> 1] |= f8_pair(bf16_lo(w[i]) / scale, bf16_hi(w[i]) / scale) << (16 * (i & 1));
+  } else {
+    const float r = 1.f / scale;
+    auto quotient = [&](float x) __attribute__((always_inline)) {
+      const float q = x * r;
+      return fmaf(fmaf(-q, scale, x), r, q);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(bf16_lo(w[2 * i])), quotient(bf16_hi(w[2 * i])), 0, false);
+      o[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(bf16_lo(w[2 * i + 1])), quotient(bf16_hi(w[2 * i + 1])), x, true);
+    }
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -198,11 +238,6 @@ __global__ __launch_bounds__(kThreads) void k_append_token(AppendArgs a, int gro
     const int lo = j0 > first ? j0 : first, hi = j0 + 8 < len ? j0 + 8 : len;
     if (n == 0 || lo >= hi) continue;
     const int page = c.table[(size_t)b * c.max_pages + (j0 >> c.page_shift)];
-    if ((unsigned)page >= (unsigned)c.n_pages) continue;
-    const int off = j0 & ((1 << c.page_shift) - 1);
-    const size_t block = ((size_t)page * c.Hkv + head) << c.page_shift;  // tokens
-    uint8_t* const kb = static_cast<uint8_t*>(a.k_pool) + block * (D + 4);
-    uint8_t* const vb = static_cast<uint8_t*>(a.v_pool) + block * (D + 4);
     const long long row0 = c.first_row(b) + (j0 - pos0);
     auto has = [&](int t) { return j0 + t >= lo && j0 + t < hi && c.has_row(row0 + t); };
     // this thread's 16 elements; a token that is not new reads the nearest row that is there
@@ -218,13 +253,23 @@ __global__ __launch_bounds__(kThreads) void k_append_token(AppendArgs a, int gro
     uint32_t kw[8], vw[8];
     load(a.k, a.k_stride, kw);
     load(a.v, a.v_stride, vw);
+    if ((unsigned)page >= (unsigned)c.n_pages) continue;
+    const int off = j0 & ((1 << c.page_shift) - 1);
+    const size_t block = ((size_t)page * c.Hkv + head) << c.page_shift;  // tokens
+    uint8_t* const kb = static_cast<uint8_t*>(a.k_pool) + block * (D + 4);
+    uint8_t* const vb = static_cast<uint8_t*>(a.v_pool) + block * (D + 4);
+    uint4* const line = reinterpret_cast<uint4*>(vb + (size_t)off * D) + at;  // 8 tokens of 2 coordinates
     bool all = true;
 #pragma unroll
     for (int i = 0; i < 8; ++i) all = all && has(i);
     uint4 old{};
-    if (!all) old = reinterpret_cast<const uint4*>(vb + (size_t)off * D)[at];
-    const float ks = token_scale<kPieces>(kw), vs = token_scale<kPieces>(vw);
-    const uint4 ke = token_entries(kw, ks), ve = token_entries(vw, vs);
+    if (!all) old = *line;
+    bool k_odd, v_odd;
+    const uint32_t k_top = token_top<kPieces>(kw, k_odd), v_top = token_top<kPieces>(vw, v_odd);
+    const float ks = token_scale(k_top), vs = token_scale(v_top);
+    const uint4 ke = token_entries(kw, ks, k_odd), ve = token_entries(vw, vs, v_odd);
+    __syncthreads();  // the last group's values are read
+    *reinterpret_cast<uint4*>(&turn[slot][t][16 * piece]) = ve;
     if (mine && has(t)) {
       reinterpret_cast<uint4*>(kb + (size_t)off * D)[at] = ke;
       if (piece == 0) {
@@ -233,21 +278,27 @@ __global__ __launch_bounds__(kThreads) void k_append_token(AppendArgs a, int gro
         reinterpret_cast<float*>(vb + scales)[off + t] = vs;
       }
     }
-    __syncthreads();  // the last group's values are read
-    *reinterpret_cast<uint4*>(&turn[slot][t][16 * piece]) = ve;
     __syncthreads();
-    uint8_t line[16];
-    __builtin_memcpy(line, &old, 16);
+    // two coordinates of a token are 16 bits; of 4 tokens the low bytes, and the high ones
+    uint32_t x[8], y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint16_t x = *reinterpret_cast<const uint16_t*>(&turn[slot][i][2 * at]);
-      const bool is = all || has(i);
-      line[i] = is ? (uint8_t)x : line[i];
-      line[8 + i] = is ? (uint8_t)(x >> 8) : line[8 + i];
+    for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint16_t*>(&turn[slot][i][2 * at]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t p = x[4 * i] | x[4 * i + 1] << 16, q = x[4 * i + 2] | x[4 * i + 3] << 16;
+      y[i] = __builtin_amdgcn_perm(q, p, 0x06040200);
+      y[2 + i] = __builtin_amdgcn_perm(q, p, 0x07050301);
     }
-    uint4 w;
-    __builtin_memcpy(&w, line, 16);
-    if (mine) reinterpret_cast<uint4*>(vb + (size_t)off * D)[at] = w;
+    if (!all) {
+      uint32_t is[2] = {0, 0};  // the new tokens' bytes
+#pragma unroll
+      for (int i = 0; i < 8; ++i) is[i >> 2] |= has(i) ? 0xFFu << (8 * (i & 3)) : 0u;
+      y[0] = (y[0] & is[0]) | (old.x & ~is[0]);
+      y[1] = (y[1] & is[1]) | (old.y & ~is[1]);
+      y[2] = (y[2] & is[0]) | (old.z & ~is[0]);
+      y[3] = (y[3] & is[1]) | (old.w & ~is[1]);
+    }
+    if (mine) *line = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 

@@ -127,13 +127,19 @@ def test_attend_depths_and_counts_out_of_range(ds):  # noqa: F811
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [3, 40])
 def test_a_chain_gives_what_a_sequence_does(ds, dtype, n):  # noqa: F811
-    # bit for bit: the same kernels and tiles
+    # Bit for bit where the kernels and their order of summation are the same (fp32, and up to 16 rows a kv head).  With
+    # more rows of bf16 a tree's waves may share their tiles: each call is within the bound of the exact value.
     c = tu.make(11, dtype, 16, 128, 8, 2, [n, n - 2], [n + 100, 77])
     parent = np.concatenate([np.arange(n) - 1, np.arange(n - 2) - 1])
-    words, _ = ot.mask(parent, c.n_new, c.row_start, len(parent), n)
+    words, depth = ot.mask(parent, c.n_new, c.row_start, len(parent), n)
     out, lse = tu.gpu_tree(ds, c, words, None)
     want, want_lse = tu.gpu_attend(ds, c)
-    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    if dtype == "f32" or n * 4 <= 16:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    else:
+        ref = tu.oracle_tree(c, words, depth)
+        tu.check(c, out, lse, ref)
+        tu.check(c, want, want_lse, ref)
 
 
 @pytest.mark.parametrize("dtype", tu.TYPES)
