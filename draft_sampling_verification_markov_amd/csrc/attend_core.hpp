@@ -81,13 +81,12 @@ struct Masks {
 // of its bits.  What every row of a tile sees is then context: depths lie between 0 and the
 // node's number.
 template <int ROWS, bool TREE>
-__device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int b, int rt) {
+__device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int b, int rt, int n, int len) {
   Geometry g;
   const int G = a.c.Hq / a.c.Hkv;
   g.b = b;
   g.row_tile = rt;
-  g.n = a.c.rows(g.b);
-  const int len = a.c.len(g.b);
+  g.n = n;
   g.pos0 = len - g.n;
   g.row0 = rt * ROWS;
   g.rows = min(ROWS, g.n * G - g.row0);
@@ -104,6 +103,11 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p
   g.tile0 = g.lo >> p.unit_shift;
   g.tiles = max(1, ((g.hi + (1 << p.unit_shift) - 1) >> p.unit_shift) - g.tile0);  // 1: its rows are written
   return g;
+}
+
+template <int ROWS, bool TREE>
+__device__ __forceinline__ Geometry geometry(const AttendArgs& a, const Split& p, int b, int rt) {
+  return geometry<ROWS, TREE>(a, p, b, rt, a.c.rows(b), a.c.len(b));
 }
 
 // The keys that a row sees: all in [lo, hi), of a tree's nodes those of its bits.
@@ -151,6 +155,7 @@ struct Start {
   long long count;  // the worker's units
   int workers;  // that have any
   long long unit, total;
+  int n, len;   // of a whole segment's request: new tokens, length
 };
 
 // Exclusive prefix over the workgroup's THREADS threads; all receives the sum.
@@ -253,25 +258,47 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
   return s;
 }
 
-// The request with the n-th largest length (of equal ones the first), by counting: every
-// thread ranks its own.  Up to kAttendThreads requests.
-__device__ __forceinline__ int nth_longest(const AttendArgs& a, int n) {
-  static_assert(kAttendThreads == 256, "a length (24 bits) and the thread's number share a word");
-  __shared__ __attribute__((aligned(16))) uint32_t key[kAttendThreads];
-  __shared__ int found;
-  const int t = threadIdx.x, B = a.c.B;
-  const int len = t < B && a.c.rows(t) > 0 ? min(a.c.len(t), (1 << 24) - 1) : 0;
-  const uint32_t mine = t < B ? ((uint32_t)len << 8) + (255 - t) : 0;
-  key[t] = mine;
-  __syncthreads();
-  int rank = 0;
-  for (int i = 0; i < B; i += 4) {  // (keys past B are 0: not larger than any)
-    const uint4 k = *reinterpret_cast<const uint4*>(key + i);
-    rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+// The request with the n-th largest length (of equal ones the first) among those with new
+// tokens, the others after them, for up to kAttendThreads requests.  Every wave holds all of
+// them, four a lane, and finds the key, a length with the request's number below it, bit by
+// bit: a bit is set where more than n keys are at least as large.  Counts are scalar, nothing
+// is shared, no wave waits for another (ranked by all threads through LDS a workgroup took 7 us
+// of its 49 for it, 256 requests of up to 17 tokens over up to 2048 keys).
+__device__ __forceinline__ int nth_longest(const AttendArgs& a, int n, int& rows, int& length) {
+  static_assert(kAttendThreads == 256, "a length (24 bits) and the request's number share a word");
+  constexpr int kEach = kAttendThreads / 64;
+  const int lane = threadIdx.x & 63, B = a.c.B;
+  uint32_t key[kEach];
+  int new_rows[kEach], len[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int t = min(64 * i + lane, B - 1);
+    new_rows[i] = a.c.rows(t);
+    len[i] = a.c.len(t);
   }
-  if (t < B && rank == n) found = t;
-  __syncthreads();
-  return found;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int t = 64 * i + lane;
+    const int l = new_rows[i] > 0 ? min(len[i], (1 << 24) - 1) : 0;
+    key[i] = t < B ? ((uint32_t)l << 8) + (255 - t) : 0;
+  }
+  uint32_t found = 0;
+#pragma unroll 4
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    int larger = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) larger += __popcll(__ballot(key[i] >= (found | bit)));
+    if (larger > n) found |= bit;
+  }
+  const int b = 255 - (int)(found & 255);
+  rows = length = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (b >> 6 == i) {
+      rows = __builtin_amdgcn_readlane(new_rows[i], b & 63);
+      length = __builtin_amdgcn_readlane(len[i], b & 63);
+    }
+  return b;
 }
 
 // The segment of a workgroup that takes a whole one (none: b = B or row_tile < 0).
@@ -288,7 +315,13 @@ __device__ __forceinline__ Start whole_segment(const AttendArgs& a, const Split&
   s.head = (int)(pair % a.c.Hkv);
   s.b = (int)(pair / a.c.Hkv);
   s.count = 0x7fffffffffffffffLL;
-  if (p.longest_first && s.b < a.c.B && s.row_tile >= 0) s.b = nth_longest(a, s.b);
+  if (s.b >= a.c.B || s.row_tile < 0) return s;
+  if (p.longest_first) {
+    s.b = nth_longest(a, s.b, s.n, s.len);
+  } else {
+    s.n = a.c.rows(s.b);
+    s.len = a.c.len(s.b);
+  }
   return s;
 }
 // workgroups of such a launch: the pairs' shares rounded up to whole rounds of the XCDs

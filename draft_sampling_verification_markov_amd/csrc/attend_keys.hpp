@@ -110,7 +110,8 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
   }
   long long left = s.count;
   bool first_segment = true;
-  Geometry g = geometry<kRows, TREE>(a, p, s.b, s.row_tile);
+  Geometry g = p.workers ? geometry<kRows, TREE>(a, p, s.b, s.row_tile)
+                         : geometry<kRows, TREE>(a, p, s.b, s.row_tile, s.n, s.len);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
   if (g.tiles == 0) return;  // a direct workgroup without rows
 
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(kAttendThreads, OCC) void k_attend_keys(AttendArgs 
     }
 
     // ---- rows
-    const Masks mask{a.causal, a.window, c.len(g.b)};
+    const Masks mask{a.causal, a.window, g.pos0 + g.n};
     const int G = c.Hq / c.Hkv;
     uint4 q[NB][TT::kQ];
     RowKeys<TREE> keys[NB];

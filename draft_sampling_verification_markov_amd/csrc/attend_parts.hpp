@@ -85,7 +85,8 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_par
   }
   long long left = s.count;
   bool first_segment = true;
-  Geometry g = geometry<kRows, TREE>(a, p, s.b, s.row_tile);
+  Geometry g = p.workers ? geometry<kRows, TREE>(a, p, s.b, s.row_tile)
+                         : geometry<kRows, TREE>(a, p, s.b, s.row_tile, s.n, s.len);
   if (p.workers && threadIdx.x == 0) put_record(partials(a, p), s, worker, g.tiles);
   if (g.tiles == 0) return;
 
@@ -107,7 +108,7 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_par
   while (true) {
     const int t0 = g.tile0 + s.skip, take = (int)min(left, (long long)(g.tiles - s.skip)), t1 = t0 + take;
     const int head = s.head;
-    const Masks mask{a.causal, a.window, c.len(g.b)};
+    const Masks mask{a.causal, a.window, g.pos0 + g.n};
     const int G = c.Hq / c.Hkv;
     const TableRow row(c, g.b);
 
