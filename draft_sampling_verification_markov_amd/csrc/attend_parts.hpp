@@ -13,7 +13,7 @@
 // - rows that several waves share.
 //
 // Of few rows and keys a segment's start counts: 2048 segments of 68 rows or less over up to
-// 2048 keys take 150 us, over up to 4096 222 (6.4 TB/s between the two), over none 39.
+// 2048 keys take 147 us (3.5 TB/s), over up to 4096 222 (6.4 TB/s between the two), over none 32.
 // (The rows' loads behind the first DMA, and a third or fourth pair of buffers, changed nothing.)
 #pragma once
 
