@@ -132,7 +132,6 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_par
     Running run{-INFINITY, 0.f};
     f32x16_t acc[S::kBlocks];
     const int rho = wrow + col;
-    // the rows, while the first tiles are on their way
     {
 #pragma unroll
       for (int db = 0; db < S::kBlocks; ++db) acc[db] = f32x16_t{};
