@@ -52,6 +52,7 @@ struct Split {
   int unit_shift;
   int spread_shift, xcd_tiles;  // of whole segments: XCDs (log2) that share a pair's row tiles, and each one's number
   bool longest_first;           // of whole segments: requests in descending order of their length
+  bool mixed;                   // of whole segments: a pair's row tiles begin at one that the pair's number picks
 };
 
 // A partial segment: O (unnormalised) [rows][D], then (m, l) [rows]; two a worker.
@@ -312,6 +313,7 @@ __device__ __forceinline__ Start whole_segment(const AttendArgs& a, const Split&
   const unsigned share = (slot / p.xcd_tiles << 3) + (blockIdx.x & 7), pair = share >> p.spread_shift;
   const int turn = (int)((slot % p.xcd_tiles << p.spread_shift) + (share & ((1u << p.spread_shift) - 1)));
   s.row_tile = p.row_tiles - 1 - turn;
+  if (p.mixed && s.row_tile >= 0) s.row_tile = (int)(((unsigned)s.row_tile + (pair * 0x9E3779B1u >> 16)) % p.row_tiles);
   s.head = (int)(pair % a.c.Hkv);
   s.b = (int)(pair / a.c.Hkv);
   s.count = 0x7fffffffffffffffLL;

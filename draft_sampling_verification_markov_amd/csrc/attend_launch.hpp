@@ -29,11 +29,19 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows
 // over 1000 52.0 / 53.4), and one prompt of 2048 rows among 255 tokens has the row tiles of
 // all of them launched (1957 us; in calls of their own 121 + 391).
+// Workgroups go round the CUs, too, so that with a pair's two row tiles in one order half of the
+// CUs get all second ones, which are small or empty where requests have different numbers of
+// rows: each pair begins at another (256 requests of up to 17 tokens x 8 query heads, 4 kv heads,
+// over up to 2048 keys, bf16 137 -> 117 us, quantised 144 -> 102; 128 trees of up to 64 nodes x 8,
+// 4 kv heads, over 3000 183 -> 152).  Prompts of a sequence, whose last row tiles see the most
+// keys, keep their order (4 x 2048 rows over up to 8192 keys 575 / 605 us).
 // Trees differ in their size, so that most of the row tiles that the largest needs are empty
 // in the others: a pair's row tiles count as two at most (8 requests of up to 256 nodes, 16
-// row tiles x 4 heads, over up to 32768 keys 1010 us whole, 252 dealt; 8 of 256, 8 x 8, over
-// 8192 151 / 85; 32 of 64, 2 x 4, over 4000 162 / 102; but 64 of 64, 2 x 8, over 4096 142 /
-// 182; 128 of 64 258 / 363).
+// row tiles x 4 heads, over up to 32768 keys 740 us whole, 239 dealt; 16 876 / 390; 8 of 256, 8
+// x 8, over 8192 154 / 82; 32 of 64, 2 x 4, over 4000 162 / 100; but 64 of 64, 2 x 8, over 4096
+// 140 / 182), as four of 128 rows over not many keys (40 of 100, 4 x 4, over 3000 82 / 97); and
+// the longest go first also where all run at once, next to short ones (64 of 128, 4 x 4, over
+// 8192 259 -> 199; 64 of 32, 1 x 8, over 8192 217 -> 193).
 // Dealt ones go to one worker a CU, or to two where there are enough keys (`twice`): the
 // second hides the other's waits, but doubles the partial results and halves their shares.
 constexpr int kFewKeys = 1024, kSomeKeys = 4096;
@@ -53,10 +61,14 @@ Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int
   pl.row_tiles = (max_rows(C, max_new) + rows - 1) / rows;
   pl.unit_shift = unit_shift;
   const long long keys = most_keys(C, max_new, window);
-  const long long pairs = (long long)C.B * C.Hkv, segments = pairs * (TREE && pl.row_tiles > 2 ? 2 : pl.row_tiles);
-  const bool direct = pairs * pl.row_tiles <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
+  const long long pairs = (long long)C.B * C.Hkv, all = pairs * pl.row_tiles;
+  const int counted = !TREE ? pl.row_tiles : rows == 128 && keys <= kSomeKeys ? 4 : 2;
+  const long long segments = pairs * (pl.row_tiles < counted ? pl.row_tiles : counted);
+  const bool direct = all <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
                                                 (!TREE && pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
-  pl.longest_first = C.B > 1 && C.B <= kAttendThreads && segments > 2 * kCUs && keys > kFewKeys && window == 0;
+  pl.longest_first = C.B > 1 && C.B <= kAttendThreads && (TREE ? all >= 2 * kCUs : all > 2 * kCUs) && keys > kFewKeys &&
+                     window == 0;
+  pl.mixed = pl.row_tiles == 2 || (TREE && pl.row_tiles > 2);
   pl.workers = direct ? 0 : per_cu > 1 && segments * keys >= r.twice ? 2 * kCUs : kCUs;
   return pl;
 }
