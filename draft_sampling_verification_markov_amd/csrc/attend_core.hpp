@@ -267,7 +267,7 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
 // of its 49 for it, 256 requests of up to 17 tokens over up to 2048 keys).
 __device__ __forceinline__ int nth_longest(const AttendArgs& a, int n, int& rows, int& length) {
   static_assert(kAttendThreads == 256, "a length (24 bits) and the request's number share a word");
-  constexpr int kEach = kAttendThreads / 64;
+  constexpr int kEach = kAttendThreads / 64, kMost = (1 << 24) - 1;
   const int lane = threadIdx.x & 63, B = a.c.B;
   uint32_t key[kEach];
   int new_rows[kEach], len[kEach];
@@ -280,12 +280,12 @@ __device__ __forceinline__ int nth_longest(const AttendArgs& a, int n, int& rows
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int t = 64 * i + lane;
-    const int l = new_rows[i] > 0 ? min(len[i], (1 << 24) - 1) : 0;
+    const int l = new_rows[i] > 0 ? min(len[i], kMost) : 0;
     key[i] = t < B ? ((uint32_t)l << 8) + (255 - t) : 0;
   }
   uint32_t found = 0;
 #pragma unroll 4
-  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+  for (uint32_t bit = 256u << (31 - __clz(min(a.c.max_pages << a.c.page_shift, kMost) | 1)); bit; bit >>= 1) {
     int larger = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) larger += __popcll(__ballot(key[i] >= (found | bit)));

@@ -23,7 +23,8 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // Whole segments of unequal length end at unequal times: where they do not all run at once,
 // the longest requests go first (100 requests of up to 17 rows over up to 3000 keys 103 ->
 // 78 us, 256 over 2048 192 -> 184, 8 x 300 rows fp32 over 2000 279 -> 230); each workgroup
-// finds its request among all, so not for few keys, nor with a window.
+// finds its request among all, 1 us or 2, so not for few keys (256 x up to 17 over up to 1000,
+// quantised, 99 -> 85, bf16 112 -> 111; over up to 500 71 -> 75), nor with a window.
 // The host knows no lengths: a segment's keys are what its request's row of the page table
 // (or the window) holds, its rows what max_new allows.  Short requests in a long table are
 // dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows
@@ -44,7 +45,7 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // 8192 259 -> 199; 64 of 32, 1 x 8, over 8192 217 -> 193).
 // Dealt ones go to one worker a CU, or to two where there are enough keys (`twice`): the
 // second hides the other's waits, but doubles the partial results and halves their shares.
-constexpr int kFewKeys = 1024, kSomeKeys = 4096;
+constexpr int kFewKeys = 1024, kSomeKeys = 4096, kOrderKeys = 768;
 struct Rule {
   int few;          // keys of a segment, of fewer than half as many as CUs (kFewKeys for more)
   long long whole;  // segments
@@ -66,7 +67,7 @@ Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int
   const long long segments = pairs * (pl.row_tiles < counted ? pl.row_tiles : counted);
   const bool direct = all <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
                                                 (!TREE && pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
-  pl.longest_first = C.B > 1 && C.B <= kAttendThreads && (TREE ? all >= 2 * kCUs : all > 2 * kCUs) && keys > kFewKeys &&
+  pl.longest_first = C.B > 1 && C.B <= kAttendThreads && (TREE ? all >= 2 * kCUs : all > 2 * kCUs) && keys > kOrderKeys &&
                      window == 0;
   pl.mixed = pl.row_tiles == 2 || (TREE && pl.row_tiles > 2);
   pl.workers = direct ? 0 : per_cu > 1 && segments * keys >= r.twice ? 2 * kCUs : kCUs;

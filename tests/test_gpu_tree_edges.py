@@ -156,3 +156,19 @@ def test_results_repeat_bit_for_bit(ds):  # noqa: F811
         _, words, depth = tu.trees(17, c)
         a, b = (tu.gpu_tree(ds, c, words, depth) for _ in range(2))
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f8t"])
+@pytest.mark.parametrize("max_pages", [96, 1 << 16])
+def test_longest_requests_first(ds, dtype, max_pages):  # noqa: F811
+    # whole segments taken in the order of their lengths, many of them equal, some of requests without new tokens; and rows
+    # of the page table as wide as they may be (2^24 tokens)
+    B, page = (256, 16) if max_pages == 96 else (130, 256)
+    i = np.arange(B)
+    length = np.where(i % 5 == 0, 40, 20 + (i * 29) % 90)
+    length[[7, B - 1]] = 1500, 1400
+    c = tu.make(18, dtype, page, 64, 16, 8 if B == 130 else 4, np.where(i % 6 == 1, 0, 1 + i % 3), length, poison=False,
+                width=max_pages)
+    _, words, depth = tu.trees(19, c)
+    tu.check(c, *tu.gpu_attend(ds, c), cu.oracle_attend(c))
+    tu.check(c, *tu.gpu_tree(ds, c, words, depth), tu.oracle_tree(c, words, depth))
