@@ -7,7 +7,7 @@
 // tile's keys and this tile's values in flight.  Blocks of 16 rows, not 32: half of the
 // registers of O and Q, so that more waves are in flight, and half of the softmax's
 // work on rows that are not there.  At a segment's end the waves' sums meet in LDS.
-// Measured: 256 tokens over up to 4096 keys, 8 heads of 128, bf16 (2.37 GB) 375 us, 6.3 TB/s;
+// Measured: 256 tokens over up to 4096 keys, 8 heads of 128, bf16 (2.37 GB) 361 us, 6.6 TB/s;
 // 2 tokens over up to 200,000 keys, 4 heads of 128, e4m3 (318 MB) 55 us and 5 for the join;
 // 256 tokens over up to 4096 keys with scales of their own (1.23 GB) 204 us, 6.0 TB/s.
 //

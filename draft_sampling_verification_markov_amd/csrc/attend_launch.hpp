@@ -29,7 +29,7 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // (or the window) holds, its rows what max_new allows.  Short requests in a long table are
 // dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows
 // over 1000 52.0 / 53.4), and one prompt of 2048 rows among 255 tokens has the row tiles of
-// all of them launched (1957 us; in calls of their own 121 + 391).
+// all of them launched (1743 us; in calls of their own 121 + 361).
 // Workgroups go round the CUs, too, so that with a pair's two row tiles in one order half of the
 // CUs get all second ones, which are small or empty where requests have different numbers of
 // rows: each pair begins at another (256 requests of up to 17 tokens x 8 query heads, 4 kv heads,
@@ -107,7 +107,7 @@ hipError_t run_keys(const dspark_cache& C, const AttendArgs& a, hipStream_t s) {
   // 108 / 111, 200 over 3000 x 8 heads 250 / 244; for more rows, 608 segments of 3000 keys,
   // 133 / 111.
   // `whole`: as many as the chip holds, where the longest go first (256 tokens over up to
-  // 4096 keys x 8 heads 375 us whole, 402 dealt; 256 over 2000 x 4, e4m3, 58 / 84); many more
+  // 4096 keys x 8 heads 361 us whole, 402 dealt; 256 over 2000 x 4, e4m3, 58 / 84); many more
   // where they cannot be ordered.
   constexpr int kHeld = (OCC > 2 ? OCC : 2) * kCUs;
   const Rule rule{CT == DSPARK_F32 && D >= 128 ? kFewKeys / 2 : kFewKeys, C.B <= kAttendThreads ? kHeld : 16 * kHeld,
