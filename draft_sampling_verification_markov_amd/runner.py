@@ -11,6 +11,7 @@ and the verification.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import numpy as np
@@ -104,12 +105,21 @@ def run_cycle(P, x: CycleInputs, o: CycleOutputs, stream=None, path: int = dspar
     verify(P, x, o, stream)
 
 
+def _on(stream):
+    """torch's operations on `stream`, or on the current one."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class PagedCache:
     """Pools, page tables, lengths and references of a paged cache, and its calls.
 
     table, length and ref are the present sequences; update writes the other set of
     them and swaps the two, compact those of table and ref (so a captured graph holds an even
-    number of updates, keep's among them, and of compactions)."""
+    number of updates, grow's and keep's among them, and of compactions).
+
+    New tokens, a tree's nodes among them, lie at the end of a sequence, and the calls over them take their number, n_new.
+    A pool without room, or the end of a row of the page table, leaves a slot fewer than were asked for: n_new is then what
+    the slot got (grow), since a larger count would take tokens that the sequence holds already for new ones."""
 
     def __init__(self, C: dspark.Cache, max_new: int, device="cuda", k_scale=None, v_scale=None):
         self.C, self.max_new = C, int(max_new)
@@ -146,6 +156,16 @@ class PagedCache:
                             self.v, self.workspace, stream)
         self._sets.reverse()
 
+    def grow(self, n_new, stream=None):
+        """Every slot longer by n_new [B] rows (clamped to [0, max_new]) as far as there is room.  Returns the rows that each
+        got, the n_new of the calls that follow, without reading anything back: none where the pool has no room (n_short
+        tells the pages that were missing), at the end of its row of the page table those that fit."""
+        self._ints(n_new=n_new)
+        with _on(stream):
+            before = self.length
+            self.update(before + n_new.clamp(0, self.max_new), stream=stream)
+            return self.length - before
+
     def compact(self, stream=None):
         """Live pages to the lowest ids (dspark_cache_compact); n_live tells how many there are."""
         now, new = self._sets
@@ -161,6 +181,11 @@ class PagedCache:
         dspark.cache_attend(self.C, layer, q, n_new, row_start, self.max_new, self.length, self.table, self.k, self.v,
                             self.k_scale, self.v_scale, out, lse, self.workspace, scale, causal, window, stream)
 
+    def _ints(self, **tensors):
+        """Refuses what is no tensor of one int32 a slot (and would be broadcast or converted)."""
+        for name, t in tensors.items():
+            dspark._dev(t, torch.int32, (self.C.B,), self.n_short.get_device(), name)
+
     # ---- drafts that form trees (dspark_tree.h); nodes are the new tokens
     def mask(self, parent, mask, depth=None, n_new=None, row_start=None, window=0, stream=None):
         """Ancestor bits and depths of the trees with these parents [rows] (dspark_tree_mask)."""
@@ -175,7 +200,15 @@ class PagedCache:
 
     def keep(self, path, n_keep, n_new=None, stream=None):
         """The accepted nodes path[b][: n_keep[b]] (ascending), and nothing else of the new tokens, stay: their keys and
-        values move to the first new places (dspark_tree_keep), and the sequences end behind them (update)."""
+        values move to the first new places (dspark_tree_keep), and the sequences end behind them (update).  With n_new a
+        path ends before the first node that is not among them: one that lost its place to a lack of room."""
+        if n_new is not None:
+            if isinstance(path, torch.Tensor) and path.dim() != 2:
+                raise ValueError(f"path has shape {tuple(path.shape)}, expected [{self.C.B}][nodes]")
+            self._ints(n_keep=n_keep, n_new=n_new)
+            dspark._dev(path, torch.int32, (self.C.B, *getattr(path, "shape", ())[1:]), self.n_short.get_device(), "path")
+            with _on(stream):
+                n_keep = torch.minimum(n_keep, (path < n_new[:, None]).sum(1, dtype=torch.int32))
         dspark.tree_keep(self.C, path, n_keep, n_new, self.max_new, self.length, self.table, self._kept, self.k, self.v,
                          stream)
         self.update(self._kept, stream=stream, n_short=self._none_short)

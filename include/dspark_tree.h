@@ -11,9 +11,16 @@
  * alone).  Node i is row row_start[b] + i, and its key and value lie at position
  * length[b] - n_new[b] + i of the request's sequence until the accepted path is kept.
  * One cycle, without the host reading anything back:
- *   dspark_cache_update (length + n_new), dspark_tree_mask,
+ *   dspark_cache_update (length + the number of nodes),
+ *   n_new = length_out - length, on the device,
+ *   dspark_tree_mask,
  *   per layer: dspark_cache_append, dspark_tree_attend,
  *   the caller's choice of a path, dspark_tree_keep, dspark_cache_update (length_out).
+ * n_new is what the update gave a request, in every call of the cycle: fewer than its nodes at
+ * the end of its row of the page table (the first nodes, a tree again), none where the pool has no
+ * room.  With a larger count the nodes would begin among the tokens that the sequence already
+ * holds: those would be overwritten, in pages that others may share, and dropped.  The path has
+ * to be cut to nodes below n_new, which in an ascending path come first.
  * A node is at position length - n_new + depth of its branch's text; encodings of
  * positions are the caller's, as they are with dspark_cache_append.
  *
@@ -74,7 +81,8 @@ dspark_status dspark_tree_attend(const dspark_cache* C, int32_t layer, const voi
  *          outside are skipped, and an order that does not ascend leaves unspecified
  *          tokens among those written; n_keep [B] int32 (clamped to [0, max_path] and to
  *          n_new[b]); n_new [B] int32 or NULL (max_new everywhere); length [B]; table
- *          [B][max_pages].
+ *          [B][max_pages].  (Entries that are skipped count in n_keep: a path that may hold nodes
+ *          that did not run is to be cut first.)
  * Outputs: length_out [B] int32, which must not overlap the inputs.
  * In/out:  k_pool, v_pool.  Pages of a request's new tokens must be its own (as after the
  *          update that made room for them).
