@@ -119,7 +119,11 @@ class PagedCache:
 
     New tokens, a tree's nodes among them, lie at the end of a sequence, and the calls over them take their number, n_new.
     A pool without room, or the end of a row of the page table, leaves a slot fewer than were asked for: n_new is then what
-    the slot got (grow), since a larger count would take tokens that the sequence holds already for new ones."""
+    the slot got (grow), since a larger count would take tokens that the sequence holds already for new ones.
+
+    max_new, of the cache, is the most new tokens of a slot in a call (its workspace is made for them).  Work is planned
+    for it, and without row_start slot b's rows begin at b * max_new, so that calls of fewer (trees, which have up to 1024
+    nodes, or single tokens, in a cache made for prompts) take a max_new of their own, the same in all that belong together."""
 
     def __init__(self, C: dspark.Cache, max_new: int, device="cuda", k_scale=None, v_scale=None):
         self.C, self.max_new = C, int(max_new)
@@ -156,14 +160,22 @@ class PagedCache:
                             self.v, self.workspace, stream)
         self._sets.reverse()
 
-    def grow(self, n_new, stream=None):
+    def _most(self, max_new):
+        """A call's max_new: the cache's, or a smaller one."""
+        if max_new is None:
+            return self.max_new
+        if not 1 <= max_new <= self.max_new:
+            raise ValueError(f"max_new {max_new} of a cache made for up to {self.max_new} new tokens a slot")
+        return max_new
+
+    def grow(self, n_new, stream=None, max_new=None):
         """Every slot longer by n_new [B] rows (clamped to [0, max_new]) as far as there is room.  Returns the rows that each
         got, the n_new of the calls that follow, without reading anything back: none where the pool has no room (n_short
         tells the pages that were missing), at the end of its row of the page table those that fit."""
         self._ints(n_new=n_new)
         with _on(stream):
             before = self.length
-            self.update(before + n_new.clamp(0, self.max_new), stream=stream)
+            self.update(before + n_new.clamp(0, self._most(max_new)), stream=stream)
             return self.length - before
 
     def compact(self, stream=None):
@@ -172,14 +184,14 @@ class PagedCache:
         dspark.cache_compact(self.C, *now, new[0], new[2], self.n_live, self.k, self.v, self.workspace, stream)
         self._sets = [(new[0], now[1], new[2]), (now[0], new[1], now[2])]
 
-    def append(self, layer: int, k, v, n_new=None, row_start=None, stream=None):
-        dspark.cache_append(self.C, layer, k, v, n_new, row_start, self.max_new, self.length, self.table,
+    def append(self, layer: int, k, v, n_new=None, row_start=None, stream=None, max_new=None):
+        dspark.cache_append(self.C, layer, k, v, n_new, row_start, self._most(max_new), self.length, self.table,
                             self.k_scale, self.v_scale, self.k, self.v, stream)
 
     def attend(self, layer: int, q, out, lse=None, n_new=None, row_start=None, scale=None, causal=True, window=0,
-               stream=None):
-        dspark.cache_attend(self.C, layer, q, n_new, row_start, self.max_new, self.length, self.table, self.k, self.v,
-                            self.k_scale, self.v_scale, out, lse, self.workspace, scale, causal, window, stream)
+               stream=None, max_new=None):
+        dspark.cache_attend(self.C, layer, q, n_new, row_start, self._most(max_new), self.length, self.table, self.k,
+                            self.v, self.k_scale, self.v_scale, out, lse, self.workspace, scale, causal, window, stream)
 
     def _ints(self, **tensors):
         """Refuses what is no tensor of one int32 a slot (and would be broadcast or converted)."""
@@ -187,21 +199,23 @@ class PagedCache:
             dspark._dev(t, torch.int32, (self.C.B,), self.n_short.get_device(), name)
 
     # ---- drafts that form trees (dspark_tree.h); nodes are the new tokens
-    def mask(self, parent, mask, depth=None, n_new=None, row_start=None, window=0, stream=None):
-        """Ancestor bits and depths of the trees with these parents [rows] (dspark_tree_mask)."""
-        if n_new is None and row_start is None and parent.numel() != self.C.B * self.max_new:
-            raise ValueError(f"{parent.numel()} parents for {self.C.B} trees of {self.max_new} nodes")
-        dspark.tree_mask(parent, n_new, row_start, self.max_new, mask, depth, window, stream)
+    def mask(self, parent, mask, depth=None, n_new=None, row_start=None, window=0, stream=None, max_new=None):
+        """Ancestor bits and depths of the trees with these parents [rows] (dspark_tree_mask: max_new up to 1024)."""
+        max_new = self._most(max_new)
+        if n_new is None and row_start is None and parent.numel() != self.C.B * max_new:
+            raise ValueError(f"{parent.numel()} parents for {self.C.B} trees of {max_new} nodes")
+        dspark.tree_mask(parent, n_new, row_start, max_new, mask, depth, window, stream)
 
     def tree_attend(self, layer: int, q, mask, out, lse=None, depth=None, n_new=None, row_start=None, scale=None, window=0,
-                    stream=None):
-        dspark.tree_attend(self.C, layer, q, n_new, row_start, self.max_new, mask, depth, self.length, self.table, self.k,
-                           self.v, self.k_scale, self.v_scale, out, lse, self.workspace, scale, window, stream)
+                    stream=None, max_new=None):
+        dspark.tree_attend(self.C, layer, q, n_new, row_start, self._most(max_new), mask, depth, self.length, self.table,
+                           self.k, self.v, self.k_scale, self.v_scale, out, lse, self.workspace, scale, window, stream)
 
-    def keep(self, path, n_keep, n_new=None, stream=None):
+    def keep(self, path, n_keep, n_new=None, stream=None, max_new=None):
         """The accepted nodes path[b][: n_keep[b]] (ascending), and nothing else of the new tokens, stay: their keys and
         values move to the first new places (dspark_tree_keep), and the sequences end behind them (update).  With n_new a
         path ends before the first node that is not among them: one that lost its place to a lack of room."""
+        max_new = self._most(max_new)
         if n_new is not None:
             if isinstance(path, torch.Tensor) and path.dim() != 2:
                 raise ValueError(f"path has shape {tuple(path.shape)}, expected [{self.C.B}][nodes]")
@@ -209,8 +223,7 @@ class PagedCache:
             dspark._dev(path, torch.int32, (self.C.B, *getattr(path, "shape", ())[1:]), self.n_short.get_device(), "path")
             with _on(stream):
                 n_keep = torch.minimum(n_keep, (path < n_new[:, None]).sum(1, dtype=torch.int32))
-        dspark.tree_keep(self.C, path, n_keep, n_new, self.max_new, self.length, self.table, self._kept, self.k, self.v,
-                         stream)
+        dspark.tree_keep(self.C, path, n_keep, n_new, max_new, self.length, self.table, self._kept, self.k, self.v, stream)
         self.update(self._kept, stream=stream, n_short=self._none_short)
 
 
