@@ -32,7 +32,9 @@
  *     tokens per lane) with one load, and a token's write stays within 8 * D elements.
  * With a scale for every token (DSPARK_F8E4M3_TOKEN) the page * D bytes of a page's head
  * are followed by the page's fp32 scales of that head, [page], in both pools: pools of
- * [n_layers][n_pages][Hkv][page * (D + 4)] bytes.
+ * [n_layers][n_pages][Hkv][page * (D + 4)] bytes.  A token that a sequence holds has finite
+ * scales, as dspark_cache_append writes them; with others the results of the rows that see the
+ * token are unspecified, and those of the rows that do not are as ever.
  * What no sequence holds (other pages, offsets past a length) may contain anything,
  * NaN and infinities included.
  *
