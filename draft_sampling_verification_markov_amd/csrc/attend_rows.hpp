@@ -190,7 +190,11 @@ __global__ __launch_bounds__(kAttendThreads, D == 256 ? 2 : 1) void k_attend_row
   while (true) {
     const int t0 = g.tile0 + s.skip, take = (int)min(left, (long long)(g.tiles - s.skip)), t1 = t0 + take;
     const int head = s.head;
-    const Masks mask{a.causal, a.window, g.pos0 + g.n};
+    // The length from memory again with e4m3, so that the tile loop's registers suffice (with g.pos0 + g.n head size 256
+    // reloads a spilled register in every tile, behind all DMA: 32 x 9 rows, window 128, 21.0 us, so 16.7; head size 64
+    // loses its order of LDS reads: 4 x 512 rows over 4096 keys 77.4, so 69.2).  bf16 is faster without (256 x 17 rows
+    // over up to 1000 keys, head size 256, 99 us, with it 104).
+    const Masks mask{a.causal, a.window, CT == DSPARK_BF16 ? g.pos0 + g.n : c.len(g.b)};
     const int G = c.Hq / c.Hkv;
     const TableRow row(c, g.b);
 
