@@ -24,7 +24,12 @@ int max_rows(const dspark_cache& C, int32_t max_new) { return max_new * (C.Hq / 
 // the longest requests go first (100 requests of up to 17 rows over up to 3000 keys 103 ->
 // 78 us, 256 over 2048 192 -> 184, 8 x 300 rows fp32 over 2000 279 -> 230); each workgroup
 // finds its request among all, 1 us or 2, so not for few keys (256 x up to 17 over up to 1000,
-// quantised, 99 -> 85, bf16 112 -> 111; over up to 500 71 -> 75), nor with a window.
+// quantised, 99 -> 85, bf16 112 -> 111; over up to 500 71 -> 75), nor with a window, nor where a
+// CU holds one workgroup at a time (fp32 of head size 256), so that nothing hides the search, with
+// four row tiles or more, which most requests leave partly empty, and more than 64 requests (in
+// order / longest first, 4 kv heads, rows x 4: 256 x up to 17 over up to 1000 keys 389 / 450, over
+// 3000 947 / 1018; 128 x 33 over 900 300 / 338; 256 x 13 over 2000 806 / 786; 256 x 20 over 900 356 /
+// 339; but three row tiles, 256 x 9 over 900 277 / 235; 64 x 17 over 1500 186 / 168).
 // The host knows no lengths: a segment's keys are what its request's row of the page table
 // (or the window) holds, its rows what max_new allows.  Short requests in a long table are
 // dealt out (16 tokens over 500 keys 11.8 us, in rows of 131072 tokens 18.8; 64 x 17 rows
@@ -68,7 +73,7 @@ Split plan_for(const dspark_cache& C, int32_t max_new, int window, int rows, int
   const bool direct = all <= (1 << 22) && (keys <= (segments < kCUs / 2 ? r.few : kFewKeys) || segments >= r.whole ||
                                                 (!TREE && pl.row_tiles > 1 && segments >= kCUs && keys <= kSomeKeys));
   pl.longest_first = C.B > 1 && C.B <= kAttendThreads && (TREE ? all >= 2 * kCUs : all > 2 * kCUs) && keys > kOrderKeys &&
-                     window == 0;
+                     window == 0 && (per_cu > 1 || pl.row_tiles < 4 || C.B <= 64);
   pl.mixed = pl.row_tiles == 2 || (TREE && pl.row_tiles > 2);
   pl.workers = direct ? 0 : per_cu > 1 && segments * keys >= r.twice ? 2 * kCUs : kCUs;
   return pl;
