@@ -264,21 +264,24 @@ __device__ __forceinline__ Start find_start(const AttendArgs& a, const Split& p,
 // them, four a lane, and finds the key, a length with the request's number below it, bit by
 // bit: a bit is set where more than n keys are at least as large.  Counts are scalar, nothing
 // is shared, no wave waits for another (ranked by all threads through LDS a workgroup took 7 us
-// of its 49 for it, 256 requests of up to 17 tokens over up to 2048 keys).
-__device__ __forceinline__ int nth_longest(const AttendArgs& a, int n, int& rows, int& length) {
-  static_assert(kAttendThreads == 256, "a length (24 bits) and the request's number share a word");
-  constexpr int kEach = kAttendThreads / 64, kMost = (1 << 24) - 1;
+// of its 49 for it, 256 requests of up to 17 tokens over up to 2048 keys).  Up to 64 requests
+// are one a lane, a quarter of the counts (8 x 300 rows over up to 2000 keys, fp32, head size
+// 256 483 -> 474 us).
+template <int EACH>
+__device__ __forceinline__ int nth_longest_of(const AttendArgs& a, int n, int& rows, int& length) {
+  static_assert(64 * EACH <= 256, "a length (24 bits) and the request's number share a word");
+  constexpr int kMost = (1 << 24) - 1;
   const int lane = threadIdx.x & 63, B = a.c.B;
-  uint32_t key[kEach];
-  int new_rows[kEach], len[kEach];
+  uint32_t key[EACH];
+  int new_rows[EACH], len[EACH];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
+  for (int i = 0; i < EACH; ++i) {
     const int t = min(64 * i + lane, B - 1);
     new_rows[i] = a.c.rows(t);
     len[i] = a.c.len(t);
   }
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
+  for (int i = 0; i < EACH; ++i) {
     const int t = 64 * i + lane;
     const int l = new_rows[i] > 0 ? min(len[i], kMost) : 0;
     key[i] = t < B ? ((uint32_t)l << 8) + (255 - t) : 0;
@@ -288,18 +291,21 @@ __device__ __forceinline__ int nth_longest(const AttendArgs& a, int n, int& rows
   for (uint32_t bit = 256u << (31 - __clz(min(a.c.max_pages << a.c.page_shift, kMost) | 1)); bit; bit >>= 1) {
     int larger = 0;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) larger += __popcll(__ballot(key[i] >= (found | bit)));
+    for (int i = 0; i < EACH; ++i) larger += __popcll(__ballot(key[i] >= (found | bit)));
     if (larger > n) found |= bit;
   }
   const int b = 255 - (int)(found & 255);
   rows = length = 0;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i)
+  for (int i = 0; i < EACH; ++i)
     if (b >> 6 == i) {
       rows = __builtin_amdgcn_readlane(new_rows[i], b & 63);
       length = __builtin_amdgcn_readlane(len[i], b & 63);
     }
   return b;
+}
+__device__ __forceinline__ int nth_longest(const AttendArgs& a, int n, int& rows, int& length) {
+  return a.c.B <= 64 ? nth_longest_of<1>(a, n, rows, length) : nth_longest_of<kAttendThreads / 64>(a, n, rows, length);
 }
 
 // The segment of a workgroup that takes a whole one (none: b = B or row_tile < 0).
