@@ -3,10 +3,11 @@
 // (attend_rows.hpp, which calls over the other types keep as it is), and
 //
 // - scales of tokens.  A key's scale is a factor of its column of scores, a value's of its
-//   weights on their way to the second product (not of their sum).  Both come by DMA next to
-//   their tiles, 64 bytes for each 16 keys.  Their products are vector instructions where the
-//   call waits for those (4 x 2048 tokens over up to 8192 keys, 32 heads reading 8 of 128: 635
-//   us, 0.93 PFLOP/s; 548 with the two products left out);
+//   weights on their way to the second product (not of their sum); the product of the two is
+//   what is rounded to bf16 there, by half a step as the weights of attend_rows.hpp, for its
+//   reason.  Both come by DMA next to their tiles, 64 bytes for each 16 keys.  Their products are
+//   vector instructions where the call waits for those (4 x 2048 tokens over up to 8192 keys, 32
+//   heads reading 8 of 128: 635 us, 0.93 PFLOP/s; 548 with the two products left out);
 // - a tree's bits in the tiles that hold its nodes (two words of the row's mask for each 32
 //   keys; 64 requests of up to 33 nodes x 4 query heads over up to 500 keys 37.0 us, as a
 //   sequence 35.1);

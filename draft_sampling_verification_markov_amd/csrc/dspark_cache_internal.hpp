@@ -1,5 +1,6 @@
-// Internal interfaces of the paged cache: argument blocks and launchers shared by
-// the ABI layer (dspark_cache_abi.hip) and the kernels (k_pages.hip, k_attend.hip).
+// Internal interfaces of the paged cache: argument blocks and launchers shared by the ABI
+// layers (dspark_cache_abi.hip, dspark_tree_abi.hip) and the kernels (k_pages.hip,
+// k_attend.hip, k_attend_tree.hip, k_tree.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
